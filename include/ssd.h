@@ -292,6 +292,128 @@ ssd_status ssd_bwd(const ssd_shape* shape, const void* x, const float* dt, const
                    const float* dfinal, void* dx, float* ddt, float* dA, void* dB, void* dC, float* dD,
                    float* dinit, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Gated linear recurrence, channels last: one state a channel, with a decay of its own for every
+ * token and channel (the first-order linear recurrence h_t = Abar_t h_{t-1} + Bbar_t x_t of "3.3
+ * Hardware-aware algorithm and GPU memory hierarchy", section 4.1, with both coefficients taken
+ * from data):
+ *     h_t = a_t h_{t-1} + u_t,   y_t = h_t          for every (batch, channel), over t < seqlen
+ *     a_t = g_t (SSD_GATE_DECAY), exp(g_t) (SSD_GATE_LOG) or 1 / (1 + exp(-g_t)) (SSD_GATE_LOGIT)
+ *     u_t = x_t, or (1 - a_t) x_t where `complement` is 1
+ *   - x, gate: (batch, seqlen, dim) in io_dtype.  Rows may be slices of wider ones: x_stride and
+ *     gate_stride are the elements from a token to the next (0: dim, dense; else >= dim), and a
+ *     batch is seqlen rows on.  Both need the alignment of their element type only; 16-byte
+ *     alignment and strides that are a multiple of 16 bytes are the fast case.
+ *   - A token with a_t = 0 (g_t = 0, -inf, -inf) starts a new sequence of a packed batch: nothing
+ *     before it reaches the states and gradients from there on.  x and the states are finite and
+ *     |a_t| <= 1 in the ordinary case; other values go through the same arithmetic, whose products
+ *     of decays over up to 4096 tokens then have to stay inside float32 range.
+ *   - y: io_dtype, dense.  init_state: float32 (batch, dim), nullable (zero state).  final_state:
+ *     float32 (batch, dim), nullable (not written).  No output may alias an input.
+ *   - states: nullable (not written); float32 (batch, ceil(seqlen / SSD_GATED_BLOCK), dim), the
+ *     state that enters each block of SSD_GATED_BLOCK tokens.  ssd_gated_scan_bwd starts from them,
+ *     so that no state of single tokens is kept for it.
+ *   - The recurrence runs in float32; y is rounded once.  No workspace; asynchronous on `stream`;
+ *     the results of a call do not depend on timing.
+ */
+typedef enum { SSD_GATE_DECAY = 0, SSD_GATE_LOG = 1, SSD_GATE_LOGIT = 2 } ssd_gate_kind;
+#define SSD_GATED_BLOCK 64
+
+typedef struct {
+  int64_t batch;       /* 1 .. 65535                                                  */
+  int64_t seqlen;      /* >= 1                                                        */
+  int64_t dim;         /* channels, 1 .. 2^20                                         */
+  int64_t x_stride;    /* elements between two tokens of x (0: dim)                   */
+  int64_t gate_stride; /* the same of gate                                            */
+  int32_t io_dtype;    /* ssd_dtype of x, gate, y, dy, dx, dgate                      */
+  int32_t kind;        /* ssd_gate_kind                                               */
+  int32_t complement;  /* 0: u = x; 1: u = (1 - a) x                                  */
+  uint32_t flags;      /* reserved, 0                                                 */
+} ssd_gated_shape;
+
+ssd_status ssd_gated_scan(const ssd_gated_shape* shape, const void* x, const void* gate,
+                          const float* init_state, void* y, float* final_state, float* states,
+                          void* stream);
+
+/*
+ * Backward pass of ssd_gated_scan, with the states recomputed on chip (section 6 of the same page):
+ *     G_t = dy_t + a_{t+1} G_{t+1}, G_{seqlen-1} = dy + dfinal        (the adjoint of h_t)
+ *     dx_t = G_t, or (1 - a_t) G_t;   da_t = G_t h_{t-1}, or G_t (h_{t-1} - x_t)
+ *     dgate_t = da_t, a_t da_t or a_t (1 - a_t) da_t;   dinit = a_0 G_0
+ *   - x, gate, dy, dx, dgate in io_dtype; dy, dx and dgate are dense.  states: what the forward pass
+ *     wrote (required; its first block is the initial state).  dfinal: float32 (batch, dim),
+ *     nullable (zero); dinit: the same shape, nullable (not written).
+ */
+ssd_status ssd_gated_scan_bwd(const ssd_gated_shape* shape, const void* x, const void* gate,
+                              const void* dy, const float* states, const float* dfinal, void* dx,
+                              void* dgate, float* dinit, void* stream);
+
+/* The same recurrence over a short run of tokens (one, for serving) on a resident state: reads
+ * state, float32 (batch, dim), and writes the state after the last token to new_state, which may be
+ * state itself (in place) but overlaps nothing else. */
+ssd_status ssd_gated_decode(const ssd_gated_shape* shape, const void* x, const void* gate,
+                            const float* state, float* new_state, void* y, void* stream);
+
+/*
+ * Group norm with an activation, channels last: x (batch, seqlen, channels), statistics over the
+ * seqlen positions and channels / ngroups channels of each (batch, group).  With seqlen = 1 and a
+ * batch of all tokens it is the norm behind a scan, one statistic for each token and group.
+ *     v = x, or x silu(z) (SSD_NORM_GATE_FIRST)
+ *     n = weight (v - mean) rstd + bias,   rstd = 1 / sqrt(mean((v - mean)^2) + eps)
+ *     y = n, silu(n) (SSD_NORM_SILU) or n silu(z) (SSD_NORM_GATE);    silu(t) = t / (1 + exp(-t))
+ * SSD_NORM_FLAG_RMS leaves the mean out (mean = 0).
+ *   - x, z, y: io_dtype.  x_stride and z_stride: elements from a position to the next (0: channels;
+ *     else >= channels), a batch is seqlen positions on; y is dense.  z is required by the two gates
+ *     and not read otherwise.  x and z need the alignment of their element type only.
+ *   - weight, bias: float32 (channels), nullable (ones, zeros).  mean, rstd: float32 (batch, ngroups),
+ *     nullable (not written); the backward pass reads them.
+ *   - workspace: ssd_norm_workspace_bytes(shape) bytes, 256-byte aligned; null where that is 0.
+ *   - Statistics are float32, taken around the mean; y is rounded once.  No output may alias an input.
+ */
+typedef enum {
+  SSD_NORM_NONE = 0,
+  SSD_NORM_SILU = 1,
+  SSD_NORM_GATE = 2,
+  SSD_NORM_GATE_FIRST = 3
+} ssd_norm_act;
+#define SSD_NORM_FLAG_RMS 1u
+
+typedef struct {
+  int64_t batch;    /* >= 1                                          */
+  int64_t seqlen;   /* positions, >= 1                               */
+  int64_t channels; /* 1 .. 2^20, a multiple of ngroups              */
+  int64_t ngroups;  /* >= 1                                          */
+  int64_t x_stride; /* elements between two positions (0: channels)  */
+  int64_t z_stride; /* the same of z                                 */
+  float eps;        /* >= 0                                          */
+  int32_t io_dtype; /* ssd_dtype of x, z, y, dy, dx, dz              */
+  int32_t act;      /* ssd_norm_act                                  */
+  uint32_t flags;   /* SSD_NORM_FLAG_*                               */
+} ssd_norm_shape;
+
+/* Workspace bytes; 0 where none is needed, and for an invalid shape (which every call rejects). */
+size_t ssd_norm_workspace_bytes(const ssd_norm_shape* shape);
+ssd_status ssd_group_norm(const ssd_norm_shape* shape, const void* x, const void* z,
+                          const float* weight, const float* bias, void* y, float* mean, float* rstd,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Backward pass of ssd_group_norm.  With dn the gradient of n, q = weight dn and xhat = (v - mean) rstd:
+ *     dv = rstd (q - mean(q) - xhat mean(q xhat))        (mean(q) left out with SSD_NORM_FLAG_RMS)
+ *     dweight = sum dn xhat,  dbias = sum dn             over batch and positions
+ *   - dy, dx, dz: io_dtype, dense.  dz is written for the two gates only (required there).
+ *   - mean, rstd: what the forward pass wrote (mean is not read, and may be null, with
+ *     SSD_NORM_FLAG_RMS).  dweight, dbias: float32 (channels), nullable (not written).
+ *   - workspace: ssd_norm_bwd_workspace_bytes(shape) bytes, 256-byte aligned; null where that is 0.
+ *   - Sums are float32 in a fixed order: the same inputs give the same bits.
+ */
+size_t ssd_norm_bwd_workspace_bytes(const ssd_norm_shape* shape);
+ssd_status ssd_group_norm_bwd(const ssd_norm_shape* shape, const void* x, const void* z,
+                              const float* weight, const float* bias, const void* dy,
+                              const float* mean, const float* rstd, void* dx, void* dz,
+                              float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
 /* Static description of a status code. */
 const char* ssd_status_str(ssd_status status);
 

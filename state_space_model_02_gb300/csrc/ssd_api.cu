@@ -642,6 +642,181 @@ ssd_status ssd_bwd(const ssd_shape* shape, const void* x, const float* dt, const
   return SSD_OK;
 }
 
+// ------------------------------------------------------- gated linear recurrence, group norm
+
+namespace {
+
+// x, gate and z may be slices of wider rows: the alignment of their elements is all they need.
+ssd_status need_elem(const void* p, bool bf16, const char* name) {
+  if (!p) return fail(SSD_ERR_INVALID, "%s is null", name);
+  if ((reinterpret_cast<uintptr_t>(p) & (bf16 ? 1u : 3u)) != 0)
+    return fail(SSD_ERR_ALIGN, "%s is not aligned to its element type", name);
+  return SSD_OK;
+}
+
+// Elements of one tensor (strides included) stay far inside int64 byte offsets.
+bool too_large(int64_t batch, int64_t rows, int64_t stride) {
+  return double(batch) * double(rows) * double(stride) > 1.0e15;
+}
+
+ssd_status make_gated(const ssd_gated_shape* s, ssd::GatedProblem* p) {
+  if (!s) return fail(SSD_ERR_INVALID, "shape is null");
+  if (s->batch < 1 || s->seqlen < 1 || s->dim < 1) return fail(SSD_ERR_INVALID, "every dimension must be >= 1");
+  if (s->io_dtype != SSD_F32 && s->io_dtype != SSD_BF16) return fail(SSD_ERR_INVALID, "bad io_dtype");
+  if (s->kind != SSD_GATE_DECAY && s->kind != SSD_GATE_LOG && s->kind != SSD_GATE_LOGIT)
+    return fail(SSD_ERR_INVALID, "bad gate kind");
+  if (s->complement != 0 && s->complement != 1) return fail(SSD_ERR_INVALID, "complement must be 0 or 1");
+  if (s->flags != 0) return fail(SSD_ERR_INVALID, "flags must be 0");
+  if ((s->x_stride != 0 && s->x_stride < s->dim) || (s->gate_stride != 0 && s->gate_stride < s->dim))
+    return fail(SSD_ERR_INVALID, "a row stride must be 0 or at least dim");
+  const int64_t sx = s->x_stride ? s->x_stride : s->dim, sg = s->gate_stride ? s->gate_stride : s->dim;
+  if (s->batch > 65535 || s->dim > (int64_t(1) << 20) || too_large(s->batch, s->seqlen, sx > sg ? sx : sg))
+    return fail(SSD_ERR_UNSUPPORTED, "dimension beyond the supported range");
+  *p = ssd::GatedProblem{s->batch, s->seqlen, s->dim, sx, sg, s->io_dtype == SSD_BF16, s->kind, s->complement == 1};
+  return SSD_OK;
+}
+
+ssd_status make_norm(const ssd_norm_shape* s, ssd::NormProblem* p) {
+  if (!s) return fail(SSD_ERR_INVALID, "shape is null");
+  if (s->batch < 1 || s->seqlen < 1 || s->channels < 1 || s->ngroups < 1)
+    return fail(SSD_ERR_INVALID, "every dimension must be >= 1");
+  if (s->channels % s->ngroups != 0) return fail(SSD_ERR_INVALID, "channels must be a multiple of ngroups");
+  if (s->io_dtype != SSD_F32 && s->io_dtype != SSD_BF16) return fail(SSD_ERR_INVALID, "bad io_dtype");
+  if (s->act < SSD_NORM_NONE || s->act > SSD_NORM_GATE_FIRST) return fail(SSD_ERR_INVALID, "bad act");
+  if (s->flags & ~SSD_NORM_FLAG_RMS) return fail(SSD_ERR_INVALID, "unknown flags");
+  if (!(s->eps >= 0.f) || s->eps > 3.0e38f) return fail(SSD_ERR_INVALID, "eps must be finite and >= 0");
+  if ((s->x_stride != 0 && s->x_stride < s->channels) || (s->z_stride != 0 && s->z_stride < s->channels))
+    return fail(SSD_ERR_INVALID, "a row stride must be 0 or at least channels");
+  const int64_t sx = s->x_stride ? s->x_stride : s->channels, sz = s->z_stride ? s->z_stride : s->channels;
+  if (s->channels > (int64_t(1) << 20) || too_large(s->batch, s->seqlen, sx > sz ? sx : sz) ||
+      s->batch > int64_t(0x7fffffff) / s->ngroups)
+    return fail(SSD_ERR_UNSUPPORTED, "dimension beyond the supported range");
+  *p = ssd::NormProblem{s->batch, s->seqlen, s->channels, s->ngroups, sx, sz, s->eps, s->io_dtype == SSD_BF16,
+                        s->act, (s->flags & SSD_NORM_FLAG_RMS) != 0};
+  return SSD_OK;
+}
+
+bool norm_gated(const ssd::NormProblem& p) { return p.act == SSD_NORM_GATE || p.act == SSD_NORM_GATE_FIRST; }
+
+ssd_status need_ws(size_t need_bytes, const void* ws, size_t ws_bytes, const char* query) {
+  if (need_bytes == 0) return SSD_OK;
+  if (!ws) return fail(SSD_ERR_WORKSPACE, "workspace is null");
+  if (ws_bytes < need_bytes) return fail(SSD_ERR_WORKSPACE, "workspace smaller than %s()", query);
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return fail(SSD_ERR_ALIGN, "workspace must be 256-byte aligned");
+  return SSD_OK;
+}
+
+}  // namespace
+
+ssd_status ssd_gated_scan(const ssd_gated_shape* shape, const void* x, const void* gate, const float* init_state,
+                          void* y, float* final_state, float* states, void* stream) {
+  ssd::GatedProblem p;
+  SSD_TRY(make_gated(shape, &p));
+  SSD_TRY(need_elem(x, p.io_bf16, "x"));
+  SSD_TRY(need_elem(gate, p.io_bf16, "gate"));
+  SSD_TRY(need(y, "y"));
+  SSD_TRY(maybe(init_state, "init_state"));
+  SSD_TRY(maybe(final_state, "final_state"));
+  SSD_TRY(maybe(states, "states"));
+  SSD_TRY(cuda_ok(ssd::launch_gated_scan(p, x, gate, init_state, y, final_state, states,
+                                         static_cast<cudaStream_t>(stream)),
+                  "gated scan launch"));
+  g_last_error[0] = '\0';
+  return SSD_OK;
+}
+
+ssd_status ssd_gated_scan_bwd(const ssd_gated_shape* shape, const void* x, const void* gate, const void* dy,
+                              const float* states, const float* dfinal, void* dx, void* dgate, float* dinit,
+                              void* stream) {
+  ssd::GatedProblem p;
+  SSD_TRY(make_gated(shape, &p));
+  SSD_TRY(need_elem(x, p.io_bf16, "x"));
+  SSD_TRY(need_elem(gate, p.io_bf16, "gate"));
+  SSD_TRY(need(dy, "dy"));
+  SSD_TRY(need(states, "states"));
+  SSD_TRY(need(dx, "dx"));
+  SSD_TRY(need(dgate, "dgate"));
+  SSD_TRY(maybe(dfinal, "dfinal"));
+  SSD_TRY(maybe(dinit, "dinit"));
+  SSD_TRY(cuda_ok(ssd::launch_gated_scan_bwd(p, x, gate, dy, states, dfinal, dx, dgate, dinit,
+                                             static_cast<cudaStream_t>(stream)),
+                  "gated scan backward launch"));
+  g_last_error[0] = '\0';
+  return SSD_OK;
+}
+
+ssd_status ssd_gated_decode(const ssd_gated_shape* shape, const void* x, const void* gate, const float* state,
+                            float* new_state, void* y, void* stream) {
+  ssd::GatedProblem p;
+  SSD_TRY(make_gated(shape, &p));
+  SSD_TRY(need_elem(x, p.io_bf16, "x"));
+  SSD_TRY(need_elem(gate, p.io_bf16, "gate"));
+  SSD_TRY(need(state, "state"));
+  SSD_TRY(need(new_state, "new_state"));
+  SSD_TRY(need(y, "y"));
+  SSD_TRY(cuda_ok(ssd::launch_gated_decode(p, x, gate, state, new_state, y, static_cast<cudaStream_t>(stream)),
+                  "gated decode launch"));
+  g_last_error[0] = '\0';
+  return SSD_OK;
+}
+
+size_t ssd_norm_workspace_bytes(const ssd_norm_shape* shape) {
+  ssd::NormProblem p;
+  return make_norm(shape, &p) == SSD_OK ? ssd::norm_workspace_bytes(p) : 0;
+}
+
+ssd_status ssd_group_norm(const ssd_norm_shape* shape, const void* x, const void* z, const float* weight,
+                          const float* bias, void* y, float* mean, float* rstd, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  ssd::NormProblem p;
+  SSD_TRY(make_norm(shape, &p));
+  SSD_TRY(need_elem(x, p.io_bf16, "x"));
+  if (norm_gated(p)) SSD_TRY(need_elem(z, p.io_bf16, "z"));
+  SSD_TRY(need(y, "y"));
+  SSD_TRY(maybe(weight, "weight"));
+  SSD_TRY(maybe(bias, "bias"));
+  SSD_TRY(maybe(mean, "mean"));
+  SSD_TRY(maybe(rstd, "rstd"));
+  SSD_TRY(need_ws(ssd::norm_workspace_bytes(p), workspace, workspace_bytes, "ssd_norm_workspace_bytes"));
+  SSD_TRY(cuda_ok(ssd::launch_group_norm(p, x, norm_gated(p) ? z : nullptr, weight, bias, y, mean, rstd, workspace,
+                                         static_cast<cudaStream_t>(stream)),
+                  "group norm launch"));
+  g_last_error[0] = '\0';
+  return SSD_OK;
+}
+
+size_t ssd_norm_bwd_workspace_bytes(const ssd_norm_shape* shape) {
+  ssd::NormProblem p;
+  return make_norm(shape, &p) == SSD_OK ? ssd::norm_bwd_workspace_bytes(p) : 0;
+}
+
+ssd_status ssd_group_norm_bwd(const ssd_norm_shape* shape, const void* x, const void* z, const float* weight,
+                              const float* bias, const void* dy, const float* mean, const float* rstd, void* dx,
+                              void* dz, float* dweight, float* dbias, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+  ssd::NormProblem p;
+  SSD_TRY(make_norm(shape, &p));
+  const bool gated = norm_gated(p);
+  SSD_TRY(need_elem(x, p.io_bf16, "x"));
+  if (gated) SSD_TRY(need_elem(z, p.io_bf16, "z"));
+  SSD_TRY(need(dy, "dy"));
+  if (!p.rms) SSD_TRY(need(mean, "mean"));
+  SSD_TRY(need(rstd, "rstd"));
+  SSD_TRY(need(dx, "dx"));
+  if (gated) SSD_TRY(need(dz, "dz"));
+  SSD_TRY(maybe(weight, "weight"));
+  SSD_TRY(maybe(bias, "bias"));
+  SSD_TRY(maybe(dweight, "dweight"));
+  SSD_TRY(maybe(dbias, "dbias"));
+  SSD_TRY(need_ws(ssd::norm_bwd_workspace_bytes(p), workspace, workspace_bytes, "ssd_norm_bwd_workspace_bytes"));
+  SSD_TRY(cuda_ok(ssd::launch_group_norm_bwd(p, x, gated ? z : nullptr, weight, bias, dy, p.rms ? nullptr : mean, rstd,
+                                             dx, gated ? dz : nullptr, dweight, dbias, workspace,
+                                             static_cast<cudaStream_t>(stream)),
+                  "group norm backward launch"));
+  g_last_error[0] = '\0';
+  return SSD_OK;
+}
+
 const char* ssd_status_str(ssd_status s) {
   switch (s) {
     case SSD_OK: return "ok";

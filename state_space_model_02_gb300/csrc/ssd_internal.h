@@ -23,6 +23,23 @@ struct SelProblem {
   bool io_bf16;
 };
 
+// Gated linear recurrence: x, gate, y (b, L, D); rows of x and gate sx and sg elements apart.
+struct GatedProblem {
+  int64_t b, L, D, sx, sg;
+  bool io_bf16;
+  int kind;         // ssd_gate_kind
+  bool complement;  // u = (1 - a) x
+};
+
+// Group norm: x, z, y (n, S, C), G groups; rows of x and z sx and sz elements apart.
+struct NormProblem {
+  int64_t n, S, C, G, sx, sz;
+  float eps;
+  bool io_bf16;
+  int act;   // ssd_norm_act
+  bool rms;  // no mean
+};
+
 // Byte offsets inside the caller's workspace.  Each region is 1024-byte aligned.
 struct Layout {
   size_t status, cs2, dtT, S, hprev, total;
@@ -118,6 +135,25 @@ bool selective_ok(const SelProblem& p);
 cudaError_t launch_selective_scan(const SelProblem& p, const void* x, const void* delta, const float* A,
                                   const void* B, const void* C, const float* Dskip, const float* init,
                                   float* final_state, void* y, cudaStream_t st);
+
+// Gated linear recurrence (gated_scan.cu): the scan, its backward pass, and a short run of tokens on a
+// resident state (new_state may be state).
+cudaError_t launch_gated_scan(const GatedProblem& p, const void* x, const void* gate, const float* init, void* y,
+                              float* final_state, float* states, cudaStream_t st);
+cudaError_t launch_gated_scan_bwd(const GatedProblem& p, const void* x, const void* gate, const void* dy,
+                                  const float* states, const float* dfinal, void* dx, void* dgate, float* dinit,
+                                  cudaStream_t st);
+cudaError_t launch_gated_decode(const GatedProblem& p, const void* x, const void* gate, const float* state,
+                                float* new_state, void* y, cudaStream_t st);
+
+// Group norm with an activation (group_norm.cu).
+size_t norm_workspace_bytes(const NormProblem& p);
+size_t norm_bwd_workspace_bytes(const NormProblem& p);
+cudaError_t launch_group_norm(const NormProblem& p, const void* x, const void* z, const float* w, const float* b,
+                              void* y, float* mean, float* rstd, void* ws, cudaStream_t st);
+cudaError_t launch_group_norm_bwd(const NormProblem& p, const void* x, const void* z, const float* w,
+                                  const float* b, const void* dy, const float* mean, const float* rstd, void* dx,
+                                  void* dz, float* dw, float* db, void* ws, cudaStream_t st);
 
 // Recurrent form over a short run of tokens (decoding); applicability by decode_ok.
 bool decode_ok(const Problem& p);

@@ -4,6 +4,7 @@ Every step of the forward scan runs in the library's CUDA kernels; PyTorch only
 provides device memory and the current stream.  If the library is missing the
 first call raises -- there is no fallback.
 """
+import contextlib
 import ctypes
 import os
 import warnings
@@ -17,6 +18,10 @@ FLAG_FORCE_SIMT = 1
 FLAG_REQUIRE_TENSOR_CORES = 2   # fail (SSD_ERR_UNSUPPORTED) rather than fall back to the CUDA cores
 FLAG_SEPARATE_STATE_PASSING = 4  # chunk_state and state_passing as two kernels (the default)
 FLAG_FUSED_STATE = 8             # the fused fwd_pass_state kernel wherever the shape allows it
+GATED_BLOCK = 64                 # tokens between two of the states that gated_scan_bwd starts from
+GATE_KINDS = {"decay": 0, "log": 1, "logit": 2}
+NORM_ACTS = {"none": 0, "silu": 1, "gate": 2, "gate_first": 3}
+NORM_FLAG_RMS = 1
 STATUS = {0: "SSD_OK", 1: "SSD_ERR_INVALID", 2: "SSD_ERR_UNSUPPORTED", 3: "SSD_ERR_ALIGN",
           4: "SSD_ERR_CUDA", 5: "SSD_ERR_TIMEOUT", 6: "SSD_ERR_WORKSPACE"}
 
@@ -25,6 +30,8 @@ EXPORTS = ("ssd_workspace_bytes", "ssd_get_workspace_layout", "ssd_fwd", "ssd_ch
            "ssd_chunk_state", "ssd_state_passing", "ssd_fwd_pass_state", "ssd_chunk_scan", "ssd_read_status",
            "ssd_selftest_wait_timeout", "ssd_fwd_noalloc", "ssd_decode", "ssd_selective_scan",
            "ssd_bwd_workspace_bytes", "ssd_bwd",
+           "ssd_gated_scan", "ssd_gated_scan_bwd", "ssd_gated_decode",
+           "ssd_norm_workspace_bytes", "ssd_group_norm", "ssd_norm_bwd_workspace_bytes", "ssd_group_norm_bwd",
            "ssd_status_str", "ssd_last_error", "ssd_kernel_plan")
 
 
@@ -37,6 +44,19 @@ class Shape(ctypes.Structure):
 class SelShape(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("dim", ctypes.c_int64),
                 ("dstate", ctypes.c_int64), ("io_dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class GatedShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("dim", ctypes.c_int64),
+                ("x_stride", ctypes.c_int64), ("gate_stride", ctypes.c_int64), ("io_dtype", ctypes.c_int32),
+                ("kind", ctypes.c_int32), ("complement", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+class NormShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64), ("channels", ctypes.c_int64),
+                ("ngroups", ctypes.c_int64), ("x_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64),
+                ("eps", ctypes.c_float), ("io_dtype", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("flags", ctypes.c_uint32)]
 
 
 class WorkspaceLayout(ctypes.Structure):
@@ -79,6 +99,13 @@ def load_library(path: str = LIB_PATH):
         "ssd_selective_scan": ([ctypes.POINTER(SelShape)] + [vp] * 10, ctypes.c_int),
         "ssd_bwd_workspace_bytes": ([sp], ctypes.c_size_t),
         "ssd_bwd": ([sp] + [vp] * 17 + [ctypes.c_size_t, vp], ctypes.c_int),
+        "ssd_gated_scan": ([ctypes.POINTER(GatedShape)] + [vp] * 7, ctypes.c_int),
+        "ssd_gated_scan_bwd": ([ctypes.POINTER(GatedShape)] + [vp] * 9, ctypes.c_int),
+        "ssd_gated_decode": ([ctypes.POINTER(GatedShape)] + [vp] * 6, ctypes.c_int),
+        "ssd_norm_workspace_bytes": ([ctypes.POINTER(NormShape)], ctypes.c_size_t),
+        "ssd_group_norm": ([ctypes.POINTER(NormShape)] + [vp] * 8 + [ctypes.c_size_t, vp], ctypes.c_int),
+        "ssd_norm_bwd_workspace_bytes": ([ctypes.POINTER(NormShape)], ctypes.c_size_t),
+        "ssd_group_norm_bwd": ([ctypes.POINTER(NormShape)] + [vp] * 12 + [ctypes.c_size_t, vp], ctypes.c_int),
         "ssd_status_str": ([ctypes.c_int], ctypes.c_char_p),
         "ssd_last_error": ([], ctypes.c_char_p),
         "ssd_kernel_plan": ([sp], ctypes.c_int),
@@ -317,6 +344,214 @@ def bwd(x, dt, A, B, C, D, dy, chunk=256, init_state=None, dfinal=None, *, works
                        _p(out["dC"]), _p(out["dD"]), _p(out["dinit"]), _p(workspace), workspace.numel(),
                        _stream(stream)))
     return out
+
+
+def _rows(t, name, like, shape):
+    """Checks t against `like`'s type and device and the three sizes of `shape`; returns the elements
+    between two of its rows (0: dense).  A slice of wider rows is taken as it lies."""
+    if not t.is_cuda or t.device != like.device:
+        raise ValueError("%s must be a CUDA tensor on x's device" % name)
+    if t.dtype != like.dtype:
+        raise TypeError("%s must be %s" % (name, like.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.is_contiguous():
+        return 0
+    n, rows, cols = shape
+    s0, s1, s2 = t.stride()
+    row = s1 if rows > 1 else s0
+    if (cols > 1 and s2 != 1) or (rows > 1 and n > 1 and s0 != rows * s1) or row < cols:
+        raise ValueError("%s must be dense, or a slice of the channels of a dense tensor" % name)
+    return row
+
+
+def _dense(t, name, like, dtype, shape):
+    if t is None:
+        return
+    if not t.is_cuda or t.device != like.device:
+        raise ValueError("%s must be a CUDA tensor on x's device" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s" % (name, dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+
+
+def _io_dtype(x):
+    torch = _torch()
+    if x.dim() != 3:
+        raise ValueError("x must have three dimensions")
+    if x.dtype == torch.bfloat16:
+        return SSD_BF16
+    if x.dtype == torch.float32:
+        return SSD_F32
+    raise TypeError("x must be bfloat16 or float32")
+
+
+def _on(x, stream):
+    """(context, stream pointer): what a call allocates inside the context belongs to the stream that its
+    kernels run on, so that memory it drops is not handed out while they still use it."""
+    torch = _torch()
+    if stream is None:
+        return contextlib.nullcontext(), ctypes.c_void_p(torch.cuda.current_stream(x.device).cuda_stream)
+    return torch.cuda.stream(stream), ctypes.c_void_p(stream.cuda_stream)
+
+
+def _gated_shape(x, gate, kind, complement):
+    io = _io_dtype(x)
+    if kind not in GATE_KINDS:
+        raise ValueError("kind must be one of %s" % ", ".join(GATE_KINDS))
+    b, L, D = x.shape
+    return GatedShape(b, L, D, _rows(x, "x", x, x.shape), _rows(gate, "gate", x, x.shape), io, GATE_KINDS[kind],
+                      1 if complement else 0, 0)
+
+
+def gated_scan(x, gate, init_state=None, *, kind="logit", complement=False, y=None, final_state=None,
+               want_final=True, want_states=False, stream=None):
+    """ssd_gated_scan: h_t = a_t h_{t-1} + u_t per channel; returns (y, final_state or None), and the states
+    that gated_scan_bwd needs as a third where ``want_states``.
+
+    x, gate (b,L,D) in one dtype (bf16 or fp32); either may be a slice of the channels of a wider dense
+    tensor.  ``kind``: a = gate ("decay"), exp(gate) ("log") or sigmoid(gate) ("logit"); u = x, or (1 - a) x
+    where ``complement``.  init_state (b,D) in fp32.  Work is enqueued on ``stream`` (default: current).
+    """
+    torch = _torch()
+    shape = _gated_shape(x, gate, kind, complement)
+    b, L, D = x.shape
+    ctx, st = _on(x, stream)
+    _dense(init_state, "init_state", x, torch.float32, (b, D))
+    states = None
+    with ctx:
+        if y is None:
+            y = torch.empty((b, L, D), dtype=x.dtype, device=x.device)
+        if final_state is None and want_final:
+            final_state = torch.empty((b, D), dtype=torch.float32, device=x.device)
+        if want_states:
+            states = torch.empty((b, -(-L // GATED_BLOCK), D), dtype=torch.float32, device=x.device)
+    _dense(y, "y", x, x.dtype, x.shape)
+    _dense(final_state, "final_state", x, torch.float32, (b, D))
+    _check(load_library().ssd_gated_scan(ctypes.byref(shape), _p(x), _p(gate), _p(init_state), _p(y),
+                                         _p(final_state), _p(states), st))
+    return (y, final_state, states) if want_states else (y, final_state)
+
+
+def gated_scan_bwd(x, gate, dy, states, dfinal=None, *, kind="logit", complement=False, stream=None):
+    """ssd_gated_scan_bwd: gradients of gated_scan given dy (and dfinal) and the ``states`` that it returned.
+    Returns a dict with dx, dgate and dinit (b,D)."""
+    torch = _torch()
+    shape = _gated_shape(x, gate, kind, complement)
+    b, L, D = x.shape
+    ctx, st = _on(x, stream)
+    _dense(dy, "dy", x, x.dtype, x.shape)
+    _dense(states, "states", x, torch.float32, (b, -(-L // GATED_BLOCK), D))
+    _dense(dfinal, "dfinal", x, torch.float32, (b, D))
+    with ctx:
+        dx = torch.empty((b, L, D), dtype=x.dtype, device=x.device)
+        dgate = torch.empty_like(dx)
+        dinit = torch.empty((b, D), dtype=torch.float32, device=x.device)
+    _check(load_library().ssd_gated_scan_bwd(ctypes.byref(shape), _p(x), _p(gate), _p(dy), _p(states), _p(dfinal),
+                                             _p(dx), _p(dgate), _p(dinit), st))
+    return dict(dx=dx, dgate=dgate, dinit=dinit)
+
+
+def gated_decode(x, gate, state, *, kind="logit", complement=False, new_state=None, y=None, stream=None):
+    """ssd_gated_decode: gated_scan over the few tokens of x (b,L,D) on a resident ``state`` (fp32, (b,D)),
+    which is updated in place, or left as it is where ``new_state`` is given.  Returns y (b,L,D)."""
+    torch = _torch()
+    shape = _gated_shape(x, gate, kind, complement)
+    b, L, D = x.shape
+    ctx, st = _on(x, stream)
+    if new_state is None:
+        new_state = state
+    _dense(state, "state", x, torch.float32, (b, D))
+    _dense(new_state, "new_state", x, torch.float32, (b, D))
+    with ctx:
+        if y is None:
+            y = torch.empty((b, L, D), dtype=x.dtype, device=x.device)
+    _dense(y, "y", x, x.dtype, x.shape)
+    _check(load_library().ssd_gated_decode(ctypes.byref(shape), _p(x), _p(gate), _p(state), _p(new_state), _p(y),
+                                           st))
+    return y
+
+
+def _norm_shape(x, z, groups, eps, act, rms):
+    io = _io_dtype(x)
+    if act not in NORM_ACTS:
+        raise ValueError("act must be one of %s" % ", ".join(NORM_ACTS))
+    gated = act in ("gate", "gate_first")
+    if gated != (z is not None):
+        raise ValueError("z goes with act='gate' and act='gate_first'")
+    n, S, C = x.shape
+    return NormShape(n, S, C, groups, _rows(x, "x", x, x.shape), _rows(z, "z", x, x.shape) if gated else 0, eps, io,
+                     NORM_ACTS[act], NORM_FLAG_RMS if rms else 0)
+
+
+def _norm_params(x, weight, bias, mean, rstd, groups):
+    torch = _torch()
+    n, _, C = x.shape
+    _dense(weight, "weight", x, torch.float32, (C,))
+    _dense(bias, "bias", x, torch.float32, (C,))
+    _dense(mean, "mean", x, torch.float32, (n, groups))
+    _dense(rstd, "rstd", x, torch.float32, (n, groups))
+
+
+def group_norm(x, weight=None, bias=None, *, groups=1, z=None, eps=1e-5, act="none", rms=False, y=None,
+               want_stats=False, stream=None):
+    """ssd_group_norm: returns y, or (y, mean, rstd) where ``want_stats`` (what group_norm_bwd needs).
+
+    x (n,S,C), channels last, bf16 or fp32: statistics over the S positions and C / groups channels of each
+    (n, group).  The norm of single tokens is x.view(tokens, 1, C).  ``act``: "none", "silu" (y = silu(norm)),
+    "gate" (y = norm * silu(z)) or "gate_first" (y = norm of x * silu(z)); ``rms`` leaves the mean out.  x and z may
+    be slices of the channels of wider dense tensors; weight, bias (C) in fp32.  Work is enqueued on ``stream``
+    (default: current).
+    """
+    torch = _torch()
+    shape = _norm_shape(x, z, groups, eps, act, rms)
+    n, S, C = x.shape
+    lib = load_library()
+    ctx, st = _on(x, stream)
+    _norm_params(x, weight, bias, None, None, groups)
+    nbytes = lib.ssd_norm_workspace_bytes(ctypes.byref(shape))
+    mean = rstd = ws = None
+    with ctx:
+        if y is None:
+            y = torch.empty((n, S, C), dtype=x.dtype, device=x.device)
+        if want_stats:
+            mean = torch.empty((n, groups), dtype=torch.float32, device=x.device)
+            rstd = torch.empty_like(mean)
+        if nbytes:
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    _dense(y, "y", x, x.dtype, x.shape)
+    _check(lib.ssd_group_norm(ctypes.byref(shape), _p(x), _p(z), _p(weight), _p(bias), _p(y), _p(mean), _p(rstd),
+                              _p(ws), nbytes, st))
+    return (y, mean, rstd) if want_stats else y
+
+
+def group_norm_bwd(x, dy, mean, rstd, weight=None, bias=None, *, groups=1, z=None, act="none", rms=False,
+                   stream=None):
+    """ssd_group_norm_bwd: gradients of group_norm given dy and the statistics that it returned.  Returns a dict
+    with dx, dz (None without z), dweight and dbias (fp32)."""
+    torch = _torch()
+    shape = _norm_shape(x, z, groups, 0.0, act, rms)
+    n, S, C = x.shape
+    lib = load_library()
+    ctx, st = _on(x, stream)
+    _dense(dy, "dy", x, x.dtype, x.shape)
+    _norm_params(x, weight, bias, mean, rstd, groups)
+    nbytes = lib.ssd_norm_bwd_workspace_bytes(ctypes.byref(shape))
+    dz = ws = None
+    with ctx:
+        dx = torch.empty((n, S, C), dtype=x.dtype, device=x.device)
+        if z is not None:
+            dz = torch.empty_like(dx)
+        dweight = torch.empty(C, dtype=torch.float32, device=x.device)
+        dbias = torch.empty_like(dweight)
+        if nbytes:
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    _check(lib.ssd_group_norm_bwd(ctypes.byref(shape), _p(x), _p(z), _p(weight), _p(bias), _p(dy), _p(mean),
+                                  _p(rstd), _p(dx), _p(dz), _p(dweight), _p(dbias), _p(ws), nbytes, st))
+    return dict(dx=dx, dz=dz, dweight=dweight, dbias=dbias)
 
 
 def chunk_cumsum(prob, dt, A, workspace, stream=None):
