@@ -90,6 +90,9 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
 // Default limit of one bounded on-chip wait (ns).
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 
+// Streaming multiprocessors of a GB300.
+constexpr int kSMs = 152;
+
 // ---- launchers (each returns the launch's cudaError_t; none synchronises) ----
 
 // chunk_cumsum stages dt tiles by TMA when chunk_cumsum_tma_ok (rows 16-byte aligned); its
