@@ -25,85 +25,127 @@ namespace {
 
 // ------------------------------------------------------------------------------ values
 
-// V neighbouring values of one token as they lie in memory
+// V neighbouring values of one token: as float32, and as they lie in memory
+template <int V>
+using vec = std::conditional_t<V == 2, float2, float>;
 template <typename IO, int V>
-struct Raw {
-  using type = std::conditional_t<sizeof(IO) * V == 2, uint16_t,
-                                  std::conditional_t<sizeof(IO) * V == 4, uint32_t, uint2>>;
-};
-template <typename IO, int V>
-using raw_t = typename Raw<IO, V>::type;
+using raw_t = std::conditional_t<sizeof(IO) * V == 2, uint16_t, std::conditional_t<sizeof(IO) * V == 4, uint32_t, uint2>>;
+
+__device__ __forceinline__ float vmul(float a, float b) { return a * b; }
+__device__ __forceinline__ float2 vmul(float2 a, float2 b) { return mul_f32x2(a, b); }
+__device__ __forceinline__ float vfma(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float2 vfma(float2 a, float2 b, float2 c) { return fma_f32x2(a, b, c); }
+__device__ __forceinline__ float vadd(float a, float b) { return a + b; }
+__device__ __forceinline__ float2 vadd(float2 a, float2 b) { return fma_f32x2(a, make_float2(1.f, 1.f), b); }
+__device__ __forceinline__ float vsub(float a, float b) { return a - b; }
+__device__ __forceinline__ float2 vsub(float2 a, float2 b) { return fma_f32x2(b, make_float2(-1.f, -1.f), a); }
+template <int V>
+__device__ __forceinline__ vec<V> splat(float f) {
+  if constexpr (V == 2)
+    return make_float2(f, f);
+  else
+    return f;
+}
 
 template <typename IO, int V>
-__device__ __forceinline__ void widen(raw_t<IO, V> r, float (&f)[V]) {
-  if constexpr (sizeof(IO) == 4 && V == 2) {
-    f[0] = __uint_as_float(r.x);
-    f[1] = __uint_as_float(r.y);
-  } else if constexpr (sizeof(IO) == 4) {
-    f[0] = __uint_as_float(r);
-  } else if constexpr (V == 2) {
-    f[0] = bf16lo_to_f32(r);
-    f[1] = bf16hi_to_f32(r);
-  } else {
-    f[0] = __uint_as_float(uint32_t(r) << 16);
-  }
+__device__ __forceinline__ vec<V> widen(raw_t<IO, V> r) {
+  if constexpr (sizeof(IO) == 4 && V == 2)
+    return make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
+  else if constexpr (sizeof(IO) == 4)
+    return __uint_as_float(r);
+  else if constexpr (V == 2)
+    return make_float2(bf16lo_to_f32(r), bf16hi_to_f32(r));
+  else
+    return __uint_as_float(uint32_t(r) << 16);
 }
 template <typename IO, int V>
-__device__ __forceinline__ raw_t<IO, V> narrow(const float (&f)[V]) {
+__device__ __forceinline__ void store(IO* p, vec<V> f) {
+  raw_t<IO, V>* q = reinterpret_cast<raw_t<IO, V>*>(p);
   if constexpr (sizeof(IO) == 4 && V == 2)
-    return make_uint2(__float_as_uint(f[0]), __float_as_uint(f[1]));
+    *q = make_uint2(__float_as_uint(f.x), __float_as_uint(f.y));
   else if constexpr (sizeof(IO) == 4)
-    return __float_as_uint(f[0]);
+    *q = __float_as_uint(f);
   else if constexpr (V == 2)
-    return pack_bf16x2(f[0], f[1]);
+    *q = pack_bf16x2(f.x, f.y);
   else
-    return static_cast<uint16_t>(pack_bf16x2(f[0], 0.f));
+    *q = static_cast<uint16_t>(pack_bf16x2(f, 0.f));
 }
 template <typename IO, int V>
 __device__ __forceinline__ raw_t<IO, V> load(const IO* p) {
   return __ldg(reinterpret_cast<const raw_t<IO, V>*>(p));
 }
+template <int V>
+__device__ __forceinline__ vec<V> load_f32(const float* p) {
+  return *reinterpret_cast<const vec<V>*>(p);
+}
+template <int V>
+__device__ __forceinline__ void store_f32(float* p, vec<V> f) {
+  *reinterpret_cast<vec<V>*>(p) = f;
+}
+
+// A raw value of each tensor for tokens behind the last one: u = 0 and a = 1 leave the state as it is, dy = 0 the
+// adjoint.
 template <typename IO, int V>
-__device__ __forceinline__ void store(IO* p, const float (&f)[V]) {
-  *reinterpret_cast<raw_t<IO, V>*>(p) = narrow<IO, V>(f);
-}
-template <int V>
-__device__ __forceinline__ void load_f32(const float* p, float (&f)[V]) {
-  if constexpr (V == 2) {
-    const float2 v = __ldg(reinterpret_cast<const float2*>(p));
-    f[0] = v.x;
-    f[1] = v.y;
-  } else {
-    f[0] = __ldg(p);
-  }
-}
-template <int V>
-__device__ __forceinline__ void store_f32(float* p, const float (&f)[V]) {
-  if constexpr (V == 2)
-    *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
+__device__ __forceinline__ raw_t<IO, V> raw_splat(uint32_t f32_bits) {
+  if constexpr (sizeof(IO) == 4 && V == 2)
+    return make_uint2(f32_bits, f32_bits);
+  else if constexpr (sizeof(IO) == 4)
+    return f32_bits;
+  else if constexpr (V == 2)
+    return f32_bits | f32_bits >> 16;
   else
-    *p = f[0];
+    return static_cast<uint16_t>(f32_bits >> 16);
+}
+template <typename IO, int V, int KIND>
+__device__ __forceinline__ raw_t<IO, V> keep_gate() {
+  return raw_splat<IO, V>(KIND == SSD_GATE_LOGIT ? 0x7f800000u : KIND == SSD_GATE_LOG ? 0u : 0x3f800000u);
+}
+
+// exp(g).  With z = g log2 e rounded, 2^z is off by |z| 2^-24 of it; bf16 results do not see that (the decays that
+// matter have small |z|, and the others' share of a state is as small as they are), float32 ones get the rounding of z
+// back to first order.  ex2 gives 0 below 2^-126; kTiny: such values keep what float32 has of them, as the square of
+// 2^(z / 2) (the gradient of a gate is proportional to its decay, however small).
+constexpr float kLog2eHi = 1.44269502f, kLog2eLo = 1.92596303e-8f, kLn2 = 0.693147181f;
+template <typename IO, bool kTiny>
+__device__ __forceinline__ float exp_of(float g) {
+  const float z = g * kLog2eHi;
+  float e = ex2(kTiny ? 0.5f * z : z);
+  if constexpr (kTiny) e *= e;
+  if constexpr (sizeof(IO) == 2) {
+    return e;
+  } else {
+    const float d = fmaf(g, kLog2eLo, fmaf(g, kLog2eHi, -z)) * kLn2;
+    return fabsf(z) < 200.f ? fmaf(e, d, e) : e;  // infinities have no remainder
+  }
 }
 
 // The decay a and s = 1 - a.  s is taken from the gate, not from a: near a = 1 the difference has lost its low
 // bits.  kS: whether s is used.
-template <int KIND, bool kS>
+template <typename IO, int KIND, bool kS, bool kTiny>
 __device__ __forceinline__ void gate_of(float g, float& a, float& s) {
   if constexpr (KIND == SSD_GATE_DECAY) {
     a = g;
     s = 1.f - g;
   } else if constexpr (KIND == SSD_GATE_LOG) {
-    a = expf(g);
+    a = exp_of<IO, kTiny>(g);
     if constexpr (kS) {
       // 1 - exp(g): for small |g| its series (the first term left out is g^6 / 5040 of it, under 5e-8)
       const float q = fmaf(g, fmaf(g, fmaf(g, fmaf(g, fmaf(g, 1.f / 720.f, 1.f / 120.f), 1.f / 24.f), 1.f / 6.f), 0.5f), 1.f);
       s = fabsf(g) < 0.25f ? -g * q : 1.f - a;
     }
-  } else {
-    const float e = expf(-fabsf(g)), r = __fdividef(1.f, 1.f + e), er = e * r;
+  } else if constexpr (kS) {
+    const float e = exp_of<IO, kTiny>(-fabsf(g)), r = __fdividef(1.f, 1.f + e), er = e * r;
     a = g >= 0.f ? r : er;
     s = g >= 0.f ? er : r;
+  } else {
+    a = __fdividef(1.f, 1.f + exp_of<IO, kTiny>(-g));
+    if (g < -80.f) a = exp_of<IO, kTiny>(g);  // 1 + exp(-g) leaves the range that the division takes
   }
+}
+template <typename IO, int KIND, bool kS, bool kTiny>
+__device__ __forceinline__ void gate_of(float2 g, float2& a, float2& s) {
+  gate_of<IO, KIND, kS, kTiny>(g.x, a.x, s.x);
+  gate_of<IO, KIND, kS, kTiny>(g.y, a.y, s.y);
 }
 
 // ------------------------------------------------------------------------------ cluster
@@ -125,6 +167,9 @@ __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void st_peer(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
+__device__ __forceinline__ void st_peer(uint32_t addr, float2 v) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.x), "f"(v.y) : "memory");
+}
 
 constexpr int kMaxCluster = 8;
 
@@ -140,8 +185,9 @@ __global__ void __launch_bounds__(NW * 32, 512 / (NW * 32)) scan_kernel(
     const ScanArgs p, const IO* __restrict__ x, const IO* __restrict__ gate, const float* __restrict__ init,
     IO* __restrict__ y, float* __restrict__ final_state, float* __restrict__ states) {
   // maps of one step, in turn for even and odd steps: a step's maps are read until the barrier of the next
-  __shared__ float warp_map[2][NW][2][V][32];
-  __shared__ float cta_map[2][kMaxCluster][2][V][32];
+  __shared__ vec<V> warp_map[2][NW][2][32];
+  __shared__ vec<V> cta_map[2][kMaxCluster][2][32];
+  __shared__ vec<V> end_state[2][32];  // after a step's last token, where the cluster is one CTA
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
   const int K = p.cluster;
   const int rank = K > 1 ? static_cast<int>(cluster_rank()) : 0;
@@ -169,6 +215,8 @@ __global__ void __launch_bounds__(NW * 32, 512 / (NW * 32)) scan_kernel(
     } else {
 #pragma unroll
       for (int i = 0; i < TW; ++i) {
+        xr[i] = raw_splat<IO, V>(0u);
+        gr[i] = keep_gate<IO, V, KIND>();
         if (t0 + i < p.L) {
           xr[i] = load<IO, V>(xp + i * p.sx);
           gr[i] = load<IO, V>(gp + i * p.sg);
@@ -177,36 +225,18 @@ __global__ void __launch_bounds__(NW * 32, 512 / (NW * 32)) scan_kernel(
     }
   };
   fetch();
-  float carry[V];  // the state that enters the cluster's step
-#pragma unroll
-  for (int v = 0; v < V; ++v) carry[v] = 0.f;
-  if (init) load_f32<V>(init + b * p.D + c, carry);
+  vec<V> carry = init ? load_f32<V>(init + b * p.D + c) : splat<V>(0.f);  // the state that enters the step
 
   for (int step = 0; step < p.steps; ++step) {
     const int par = step & 1;
-    float a[TW][V], u[TW][V], P[V], H[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      P[v] = 1.f;
-      H[v] = 0.f;
-    }
+    vec<V> a[TW], u[TW], s, P = splat<V>(1.f), H = splat<V>(0.f);
 #pragma unroll
     for (int i = 0; i < TW; ++i) {
-      const bool in = t0 + i < p.L;  // a token behind the last one leaves the state as it is
-      float g[V], s;
-      widen<IO, V>(gr[i], g);
-      widen<IO, V>(xr[i], u[i]);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        gate_of<KIND, COMP>(g[v], a[i][v], s);
-        if constexpr (COMP) u[i][v] *= s;
-        if (!in) {
-          a[i][v] = 1.f;
-          u[i][v] = 0.f;
-        }
-        H[v] = fmaf(a[i][v], H[v], u[i][v]);
-        P[v] *= a[i][v];
-      }
+      gate_of<IO, KIND, COMP, false>(widen<IO, V>(gr[i]), a[i], s);
+      u[i] = widen<IO, V>(xr[i]);
+      if constexpr (COMP) u[i] = vmul(u[i], s);
+      H = vfma(a[i], H, u[i]);
+      P = vmul(P, a[i]);
     }
     const int64_t now = t0;
     t0 += span;
@@ -214,61 +244,60 @@ __global__ void __launch_bounds__(NW * 32, 512 / (NW * 32)) scan_kernel(
     gp += span * p.sg;
     if (step + 1 < p.steps) fetch();
 
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      warp_map[par][w][0][v][lane] = P[v];
-      warp_map[par][w][1][v][lane] = H[v];
-    }
+    warp_map[par][w][0][lane] = P;
+    warp_map[par][w][1][lane] = H;
     __syncthreads();
+    vec<V> h;
     if (K > 1) {
-      if (w < K) {  // warp w tells CTA w
+      if (w == 0) {  // the CTA's own map, to every CTA of the cluster
+        vec<V> cp = warp_map[par][0][0][lane], ch = warp_map[par][0][1][lane];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          float cp = 1.f, ch = 0.f;
-#pragma unroll
-          for (int k = 0; k < NW; ++k) {
-            const float kp = warp_map[par][k][0][v][lane];
-            ch = fmaf(kp, ch, warp_map[par][k][1][v][lane]);
-            cp *= kp;
-          }
-          st_peer(peer_addr(smem_u32(&cta_map[par][rank][0][v][lane]), w), cp);
-          st_peer(peer_addr(smem_u32(&cta_map[par][rank][1][v][lane]), w), ch);
+        for (int k = 1; k < NW; ++k) {
+          const vec<V> kp = warp_map[par][k][0][lane];
+          ch = vfma(kp, ch, warp_map[par][k][1][lane]);
+          cp = vmul(cp, kp);
+        }
+        for (int k = 0; k < K; ++k) {
+          st_peer(peer_addr(smem_u32(&cta_map[par][rank][0][lane]), k), cp);
+          st_peer(peer_addr(smem_u32(&cta_map[par][rank][1][lane]), k), ch);
         }
       }
       cluster_sync();
-    }
-    float h[V];
+      h = carry;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      h[v] = carry[v];
-      if (K > 1) {
-        for (int k = 0; k < K; ++k) {
-          if (k == rank) h[v] = carry[v];
-          carry[v] = fmaf(cta_map[par][k][0][v][lane], carry[v], cta_map[par][k][1][v][lane]);
-        }
+      for (int k = 0; k < kMaxCluster; ++k) {
+        if (k == rank) h = carry;
+        if (k < K) carry = vfma(cta_map[par][k][0][lane], carry, cta_map[par][k][1][lane]);
       }
+    } else {
+      if (step > 0) carry = end_state[par][lane];
+      h = carry;
     }
 #pragma unroll
-    for (int k = 0; k < NW; ++k) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float kp = warp_map[par][k][0][v][lane], kh = warp_map[par][k][1][v][lane];
-        if (k < w) h[v] = fmaf(kp, h[v], kh);
-        if (K == 1) carry[v] = fmaf(kp, carry[v], kh);
-      }
-    }
+    for (int k = 0; k < NW - 1; ++k)
+      if (k < w) h = vfma(warp_map[par][k][0][lane], h, warp_map[par][k][1][lane]);
     if (states && now % SSD_GATED_BLOCK == 0 && now < p.L && mine)
       store_f32<V>(states + (b * blocks + now / SSD_GATED_BLOCK) * p.D + c, h);
-    const bool full = now + TW <= p.L;
+    if (mine && now + TW <= p.L) {
 #pragma unroll
-    for (int i = 0; i < TW; ++i) {
+      for (int i = 0; i < TW; ++i) {
+        h = vfma(a[i], h, u[i]);
+        store<IO, V>(yp + i * p.D, h);
+      }
+    } else {
 #pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = fmaf(a[i][v], h[v], u[i][v]);
-      if (mine && (full || now + i < p.L)) store<IO, V>(yp + i * p.D, h);
+      for (int i = 0; i < TW; ++i) {
+        h = vfma(a[i], h, u[i]);
+        if (mine && now + i < p.L) store<IO, V>(yp + i * p.D, h);
+      }
     }
     yp += span * p.D;
+    if (K == 1 && w == NW - 1) {
+      carry = h;
+      end_state[par ^ 1][lane] = h;
+    }
   }
-  if (final_state && rank == 0 && w == 0 && mine) store_f32<V>(final_state + b * p.D + c, carry);
+  if (final_state && rank == 0 && w == NW - 1 && mine) store_f32<V>(final_state + b * p.D + c, carry);
   if (K > 1) cluster_sync();  // no CTA leaves while another may still write to its shared memory
   grid_dep_launch();
 }
@@ -286,31 +315,20 @@ __global__ void __launch_bounds__(128) run_kernel(const ScanArgs p, const IO* __
   const IO* xp = x + b * p.L * p.sx + c;
   const IO* gp = gate + b * p.L * p.sg + c;
   IO* yp = y + b * p.L * p.D + c;
-  float h[V] = {};
-  if (init) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = init[b * p.D + c + v];
-  }
+  vec<V> h = init ? load_f32<V>(init + b * p.D + c) : splat<V>(0.f);
 #pragma unroll 4
   for (int64_t t = 0; t < p.L; ++t) {
     if (states && t % SSD_GATED_BLOCK == 0) store_f32<V>(states + (b * blocks + t / SSD_GATED_BLOCK) * p.D + c, h);
-    float xv[V], g[V], a, s;
-    widen<IO, V>(load<IO, V>(xp), xv);
-    widen<IO, V>(load<IO, V>(gp), g);
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      gate_of<KIND, COMP>(g[v], a, s);
-      h[v] = fmaf(a, h[v], COMP ? s * xv[v] : xv[v]);
-    }
+    vec<V> u = widen<IO, V>(load<IO, V>(xp)), a, s;
+    gate_of<IO, KIND, COMP, false>(widen<IO, V>(load<IO, V>(gp)), a, s);
+    if constexpr (COMP) u = vmul(u, s);
+    h = vfma(a, h, u);
     store<IO, V>(yp, h);
     xp += p.sx;
     gp += p.sg;
     yp += p.D;
   }
-  if (final_state) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) final_state[b * p.D + c + v] = h[v];
-  }
+  if (final_state) store_f32<V>(final_state + b * p.D + c, h);
   grid_dep_launch();
 }
 
@@ -329,8 +347,9 @@ __global__ void __launch_bounds__(NW * 32, 512 / (NW * 32)) scan_bwd_kernel(
     float* __restrict__ dinit) {
   static_assert(NW * TW == SSD_GATED_BLOCK, "a CTA's tile is a block");
   constexpr bool kS = COMP || KIND == SSD_GATE_LOGIT;
-  __shared__ float warp_map[2][NW][3][V][32];
-  __shared__ float cta_map[2][kMaxCluster][2][V][32];
+  __shared__ vec<V> warp_map[2][NW][3][32];
+  __shared__ vec<V> cta_map[2][kMaxCluster][2][32];
+  __shared__ vec<V> end_adjoint[2][32];  // what leaves a step's first token, where the cluster is one CTA
   const int lane = threadIdx.x % 32, w = threadIdx.x / 32;
   const int K = p.cluster;
   const int rank = K > 1 ? static_cast<int>(cluster_rank()) : 0;
@@ -345,7 +364,7 @@ __global__ void __launch_bounds__(NW * 32, 512 / (NW * 32)) scan_bwd_kernel(
   if (K > 1) cluster_sync();
   grid_dep_wait();
   raw_t<IO, V> xr[TW], gr[TW], dr[TW];
-  float hr[V];
+  vec<V> hr = splat<V>(0.f);
   auto fetch = [&]() {
     const IO* xp = x + (b * p.L + t0) * p.sx + c;
     const IO* gp = gate + (b * p.L + t0) * p.sg + c;
@@ -360,6 +379,9 @@ __global__ void __launch_bounds__(NW * 32, 512 / (NW * 32)) scan_bwd_kernel(
     } else {
 #pragma unroll
       for (int i = 0; i < TW; ++i) {
+        xr[i] = raw_splat<IO, V>(0u);
+        gr[i] = keep_gate<IO, V, KIND>();
+        dr[i] = raw_splat<IO, V>(0u);
         if (t0 + i < p.L) {
           xr[i] = load<IO, V>(xp + i * p.sx);
           gr[i] = load<IO, V>(gp + i * p.sg);
@@ -367,130 +389,89 @@ __global__ void __launch_bounds__(NW * 32, 512 / (NW * 32)) scan_bwd_kernel(
         }
       }
     }
-    if (block < blocks) load_f32<V>(states + (b * blocks + block) * p.D + c, hr);
+    if (block < blocks) hr = load_f32<V>(states + (b * blocks + block) * p.D + c);
   };
-#pragma unroll
-  for (int v = 0; v < V; ++v) hr[v] = 0.f;
   fetch();
-  float carry[V];  // what the tokens right of the cluster's step send to its last state
-#pragma unroll
-  for (int v = 0; v < V; ++v) carry[v] = 0.f;
-  if (dfinal) load_f32<V>(dfinal + b * p.D + c, carry);
+  vec<V> carry = dfinal ? load_f32<V>(dfinal + b * p.D + c) : splat<V>(0.f);  // what enters the step from its right
 
   for (int step = p.steps - 1; step >= 0; --step) {
     const int par = step & 1;
-    float a[TW][V], s[TW][V], u[TW][V], xv[TW][V], d[TW][V], P[V], H[V], R[V], h[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      P[v] = 1.f;
-      H[v] = 0.f;
-      R[v] = 0.f;
-      h[v] = hr[v];
-    }
+    vec<V> a[TW], s[TW], xv[TW], d[TW], P = splat<V>(1.f), H = splat<V>(0.f), R = splat<V>(0.f), h = hr;
 #pragma unroll
     for (int i = 0; i < TW; ++i) {
-      const bool in = t0 + i < p.L;
-      float g[V];
-      widen<IO, V>(gr[i], g);
-      widen<IO, V>(xr[i], xv[i]);
-      widen<IO, V>(dr[i], d[i]);
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        gate_of<KIND, kS>(g[v], a[i][v], s[i][v]);
-        u[i][v] = COMP ? s[i][v] * xv[i][v] : xv[i][v];
-        if (!in) {
-          a[i][v] = 1.f;
-          u[i][v] = 0.f;
-          d[i][v] = 0.f;
-        }
-        H[v] = fmaf(a[i][v], H[v], u[i][v]);
-        P[v] *= a[i][v];
-      }
+      gate_of<IO, KIND, kS, true>(widen<IO, V>(gr[i]), a[i], s[i]);
+      xv[i] = widen<IO, V>(xr[i]);
+      d[i] = widen<IO, V>(dr[i]);
+      H = vfma(a[i], H, COMP ? vmul(xv[i], s[i]) : xv[i]);
+      P = vmul(P, a[i]);
     }
 #pragma unroll
-    for (int i = TW - 1; i >= 0; --i) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) R[v] = a[i][v] * (d[i][v] + R[v]);
-    }
+    for (int i = TW - 1; i >= 0; --i) R = vmul(a[i], vadd(d[i], R));
     const int64_t now = t0;
     block -= K;
     t0 -= int64_t(K) * SSD_GATED_BLOCK;
     if (step > 0) fetch();
 
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      warp_map[par][w][0][v][lane] = P[v];
-      warp_map[par][w][1][v][lane] = H[v];
-      warp_map[par][w][2][v][lane] = R[v];
-    }
+    warp_map[par][w][0][lane] = P;
+    warp_map[par][w][1][lane] = H;
+    warp_map[par][w][2][lane] = R;
     __syncthreads();
+    vec<V> q;  // what the tokens right of this warp's send to its last state
     if (K > 1) {
-      if (w < K) {
+      if (w == 0) {
+        vec<V> cp = warp_map[par][NW - 1][0][lane], cr = warp_map[par][NW - 1][2][lane];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          float cp = 1.f, cr = 0.f;
-#pragma unroll
-          for (int k = NW - 1; k >= 0; --k) {
-            const float kp = warp_map[par][k][0][v][lane];
-            cr = fmaf(kp, cr, warp_map[par][k][2][v][lane]);
-            cp *= kp;
-          }
-          st_peer(peer_addr(smem_u32(&cta_map[par][rank][0][v][lane]), w), cp);
-          st_peer(peer_addr(smem_u32(&cta_map[par][rank][1][v][lane]), w), cr);
+        for (int k = NW - 2; k >= 0; --k) {
+          const vec<V> kp = warp_map[par][k][0][lane];
+          cr = vfma(kp, cr, warp_map[par][k][2][lane]);
+          cp = vmul(cp, kp);
+        }
+        for (int k = 0; k < K; ++k) {
+          st_peer(peer_addr(smem_u32(&cta_map[par][rank][0][lane]), k), cp);
+          st_peer(peer_addr(smem_u32(&cta_map[par][rank][1][lane]), k), cr);
         }
       }
       cluster_sync();
-    }
-    float q[V];  // what the tokens right of this warp's send to its last state
+      q = carry;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      q[v] = carry[v];
-      if (K > 1) {
-        for (int k = K - 1; k >= 0; --k) {
-          if (k == rank) q[v] = carry[v];
-          carry[v] = fmaf(cta_map[par][k][0][v][lane], carry[v], cta_map[par][k][1][v][lane]);
-        }
+      for (int k = kMaxCluster - 1; k >= 0; --k) {
+        if (k == rank) q = carry;
+        if (k < K) carry = vfma(cta_map[par][k][0][lane], carry, cta_map[par][k][1][lane]);
       }
+    } else {
+      if (step + 1 < p.steps) carry = end_adjoint[par][lane];
+      q = carry;
     }
 #pragma unroll
-    for (int k = 0; k < NW; ++k) {
+    for (int k = 0; k < NW - 1; ++k) {
       const int r = NW - 1 - k;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (k < w) h[v] = fmaf(warp_map[par][k][0][v][lane], h[v], warp_map[par][k][1][v][lane]);
-        const float kp = warp_map[par][r][0][v][lane], kr = warp_map[par][r][2][v][lane];
-        if (r > w) q[v] = fmaf(kp, q[v], kr);
-        if (K == 1) carry[v] = fmaf(kp, carry[v], kr);
-      }
+      if (k < w) h = vfma(warp_map[par][k][0][lane], h, warp_map[par][k][1][lane]);
+      if (r > w) q = vfma(warp_map[par][r][0][lane], q, warp_map[par][r][2][lane]);
     }
-    // u becomes what da multiplies: the state that the token starts from, less x with the complement
+    // x becomes what da multiplies: the state that the token starts from, less x with the complement
 #pragma unroll
     for (int i = 0; i < TW; ++i) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float was = h[v];
-        h[v] = fmaf(a[i][v], was, u[i][v]);
-        u[i][v] = COMP ? was - xv[i][v] : was;
-      }
+      const vec<V> was = h;
+      h = vfma(a[i], was, COMP ? vmul(xv[i], s[i]) : xv[i]);
+      xv[i] = COMP ? vsub(was, xv[i]) : was;
     }
-    const bool full = now + TW <= p.L;
+    const bool full = mine && now + TW <= p.L;
     IO* dxp = dx + (b * p.L + now) * p.D + c;
     IO* dgp = dgate + (b * p.L + now) * p.D + c;
 #pragma unroll
     for (int i = TW - 1; i >= 0; --i) {
-      float ox[V], og[V];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float G = d[i][v] + q[v];
-        q[v] = a[i][v] * G;
-        ox[v] = COMP ? G * s[i][v] : G;
-        og[v] = KIND == SSD_GATE_DECAY ? G * u[i][v] : q[v] * u[i][v];
-        if constexpr (KIND == SSD_GATE_LOGIT) og[v] *= s[i][v];
-      }
-      if (mine && (full || now + i < p.L)) {
-        store<IO, V>(dxp + i * p.D, ox);
+      const vec<V> G = vadd(d[i], q);
+      q = vmul(a[i], G);
+      vec<V> og = vmul(KIND == SSD_GATE_DECAY ? G : q, xv[i]);
+      if constexpr (KIND == SSD_GATE_LOGIT) og = vmul(og, s[i]);
+      if (full || (mine && now + i < p.L)) {
+        store<IO, V>(dxp + i * p.D, COMP ? vmul(G, s[i]) : G);
         store<IO, V>(dgp + i * p.D, og);
       }
+    }
+    if (K == 1 && w == 0) {
+      carry = q;
+      end_adjoint[par ^ 1][lane] = q;
     }
   }
   if (dinit && rank == 0 && w == 0 && mine) store_f32<V>(dinit + b * p.D + c, carry);
