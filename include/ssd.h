@@ -307,14 +307,15 @@ ssd_status ssd_bwd(const ssd_shape* shape, const void* x, const float* dt, const
  *   - A token with a_t = 0 (g_t = 0, -inf, -inf) starts a new sequence of a packed batch: nothing
  *     before it reaches the states and gradients from there on.  x and the states are finite and
  *     |a_t| <= 1 in the ordinary case; other values go through the same arithmetic, whose products
- *     of decays over up to 4096 tokens then have to stay inside float32 range.
+ *     of decays over runs of tokens (up to a whole sequence) then have to stay inside float32 range.
  *   - y: io_dtype, dense.  init_state: float32 (batch, dim), nullable (zero state).  final_state:
  *     float32 (batch, dim), nullable (not written).  No output may alias an input.
  *   - states: nullable (not written); float32 (batch, ceil(seqlen / SSD_GATED_BLOCK), dim), the
  *     state that enters each block of SSD_GATED_BLOCK tokens.  ssd_gated_scan_bwd starts from them,
  *     so that no state of single tokens is kept for it.
- *   - The recurrence runs in float32; y is rounded once.  No workspace; asynchronous on `stream`;
- *     the results of a call do not depend on timing.
+ *   - workspace: ssd_gated_workspace_bytes(shape) bytes, 256-byte aligned; null where that is 0.
+ *   - The recurrence runs in float32; y is rounded once.  Asynchronous on `stream`; the results of a
+ *     call do not depend on timing.
  */
 typedef enum { SSD_GATE_DECAY = 0, SSD_GATE_LOG = 1, SSD_GATE_LOGIT = 2 } ssd_gate_kind;
 #define SSD_GATED_BLOCK 64
@@ -331,9 +332,11 @@ typedef struct {
   uint32_t flags;      /* reserved, 0                                                 */
 } ssd_gated_shape;
 
+/* Workspace bytes; 0 where none is needed, and for an invalid shape (which every call rejects). */
+size_t ssd_gated_workspace_bytes(const ssd_gated_shape* shape);
 ssd_status ssd_gated_scan(const ssd_gated_shape* shape, const void* x, const void* gate,
                           const float* init_state, void* y, float* final_state, float* states,
-                          void* stream);
+                          void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Backward pass of ssd_gated_scan, with the states recomputed on chip (section 6 of the same page):
@@ -343,10 +346,13 @@ ssd_status ssd_gated_scan(const ssd_gated_shape* shape, const void* x, const voi
  *   - x, gate, dy, dx, dgate in io_dtype; dy, dx and dgate are dense.  states: what the forward pass
  *     wrote (required; its first block is the initial state).  dfinal: float32 (batch, dim),
  *     nullable (zero); dinit: the same shape, nullable (not written).
+ *   - workspace: ssd_gated_bwd_workspace_bytes(shape) bytes, 256-byte aligned; null where that is 0.
  */
+size_t ssd_gated_bwd_workspace_bytes(const ssd_gated_shape* shape);
 ssd_status ssd_gated_scan_bwd(const ssd_gated_shape* shape, const void* x, const void* gate,
                               const void* dy, const float* states, const float* dfinal, void* dx,
-                              void* dgate, float* dinit, void* stream);
+                              void* dgate, float* dinit, void* workspace, size_t workspace_bytes,
+                              void* stream);
 
 /* The same recurrence over a short run of tokens (one, for serving) on a resident state: reads
  * state, float32 (batch, dim), and writes the state after the last token to new_state, which may be

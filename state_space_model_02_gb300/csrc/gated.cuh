@@ -1,0 +1,363 @@
+// gated.cuh -- what the gated linear recurrence's kernels share: the gates, float32 pairs, the per-warp rings of
+// shared memory that tokens arrive in, and the exchange of maps inside a cluster.
+#pragma once
+#include <type_traits>
+
+#include "ptx.cuh"
+#include "ssd.h"
+#include "ssd_internal.h"
+
+namespace ssd {
+namespace gated {
+
+constexpr int kMaxCluster = 8;  // CTAs along the sequence
+
+// One launch.  A column's sequence is cut into `segments` runs of seg_len tokens; a cluster of CTAs walks one of them
+// in `steps` steps.
+struct Args {
+  int64_t L, D, sx, sg;
+  int64_t seg_len;
+  int cluster, steps, segments;
+};
+
+// ------------------------------------------------------------------------------ values
+
+__device__ __forceinline__ float2 vadd(float2 a, float2 b) { return fma_f32x2(a, make_float2(1.f, 1.f), b); }
+__device__ __forceinline__ float2 vsub(float2 a, float2 b) { return fma_f32x2(b, make_float2(-1.f, -1.f), a); }
+// A step of a chain: two single operations, whose latency is below a packed one's.
+__device__ __forceinline__ float2 chain_fma(float2 a, float2 b, float2 c) {
+  return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y));
+}
+__device__ __forceinline__ float2 chain_mul(float2 a, float2 b) { return make_float2(a.x * b.x, a.y * b.y); }
+
+// Two neighbouring values as they lie in memory
+template <typename IO>
+using pair_t = std::conditional_t<sizeof(IO) == 2, uint32_t, float2>;
+
+__device__ __forceinline__ float2 widen(uint32_t r) { return make_float2(bf16lo_to_f32(r), bf16hi_to_f32(r)); }
+__device__ __forceinline__ float2 widen(float2 r) { return r; }
+__device__ __forceinline__ float widen(uint16_t r) { return __uint_as_float(uint32_t(r) << 16); }
+__device__ __forceinline__ float widen(float r) { return r; }
+__device__ __forceinline__ void narrow(uint32_t& r, float2 f) { r = pack_bf16x2(f.x, f.y); }
+__device__ __forceinline__ void narrow(float2& r, float2 f) { r = f; }
+
+// Float32 values of a lane's two channels c and c + 1 in a row of D; a row of odd length starts at any multiple of
+// four bytes.
+__device__ __forceinline__ float2 load_row(const float* row, int64_t c, int64_t D) {
+  if (D % 2 == 0) return c < D ? *reinterpret_cast<const float2*>(row + c) : make_float2(0.f, 0.f);
+  return make_float2(c < D ? row[c] : 0.f, c + 1 < D ? row[c + 1] : 0.f);
+}
+__device__ __forceinline__ void store_row(float* row, int64_t c, int64_t D, float2 f) {
+  if (D % 2 == 0) {
+    if (c < D) *reinterpret_cast<float2*>(row + c) = f;
+  } else {
+    if (c < D) row[c] = f.x;
+    if (c + 1 < D) row[c + 1] = f.y;
+  }
+}
+
+// 1 / v on the MUFU unit, for v >= 1 (0 above 2^126)
+__device__ __forceinline__ float rcp(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// exp(g).  With z = g log2 e rounded, 2^z is off by |z| 2^-24 of it; bf16 results do not see that (the decays that
+// matter have small |z|, and the others' share of a state is as small as they are), float32 ones get the rounding of z
+// back to first order.  ex2 gives 0 below 2^-126; kTiny: such values keep what float32 has of them, as the square of
+// 2^(z / 2) (the gradient of a gate is proportional to its decay, however small).
+constexpr float kLog2eHi = 1.44269502f, kLog2eLo = 1.92596303e-8f, kLn2 = 0.693147181f;
+template <typename IO, bool kTiny>
+__device__ __forceinline__ float exp_of(float g) {
+  if constexpr (sizeof(IO) == 2) {
+    const float e = ex2(g * (kTiny ? 0.5f * kLog2eHi : kLog2eHi));
+    return kTiny ? e * e : e;
+  } else {
+    const float z = g * kLog2eHi;
+    float e = ex2(kTiny ? 0.5f * z : z);
+    if constexpr (kTiny) e *= e;
+    const float d = fmaf(g, kLog2eLo, fmaf(g, kLog2eHi, -z)) * kLn2;
+    return fabsf(z) < 200.f ? fmaf(e, d, e) : e;  // infinities have no remainder
+  }
+}
+
+// The decay a and s = 1 - a.  s is taken from the gate, not from a: near a = 1 the difference has lost its low
+// bits.  kS: whether s is used.
+template <typename IO, int KIND, bool kS, bool kTiny>
+__device__ __forceinline__ void gate_of(float g, float& a, float& s) {
+  if constexpr (KIND == SSD_GATE_DECAY) {
+    a = g;
+    s = 1.f - g;
+  } else if constexpr (KIND == SSD_GATE_LOG) {
+    a = exp_of<IO, kTiny>(g);
+    if constexpr (kS) {
+      // 1 - exp(g): for small |g| its series (the first term left out is g^6 / 5040 of it, under 5e-8)
+      const float q = fmaf(g, fmaf(g, fmaf(g, fmaf(g, fmaf(g, 1.f / 720.f, 1.f / 120.f), 1.f / 24.f), 1.f / 6.f), 0.5f), 1.f);
+      s = fabsf(g) < 0.25f ? -g * q : 1.f - a;
+    }
+  } else {
+    const float e = exp_of<IO, kTiny>(-g);
+    a = rcp(1.f + e);
+    if constexpr (kS) s = e > 1.f ? 1.f - a : e * a;
+  }
+}
+template <typename IO, int KIND, bool kS, bool kTiny>
+__device__ __forceinline__ void gate_of(float2 g, float2& a, float2& s) {
+  if constexpr (KIND == SSD_GATE_LOGIT && sizeof(IO) == 2) {  // the same, two at a time where the pipes can
+    constexpr float kScale = (kTiny ? -0.5f : -1.f) * kLog2eHi;
+    const float2 z = mul_f32x2(g, make_float2(kScale, kScale));
+    float2 e = make_float2(ex2(z.x), ex2(z.y));
+    if constexpr (kTiny) e = mul_f32x2(e, e);
+    const float2 d = vadd(e, make_float2(1.f, 1.f));
+    a = make_float2(rcp(d.x), rcp(d.y));
+    if constexpr (kS) {
+      const float2 ea = mul_f32x2(e, a), na = vsub(make_float2(1.f, 1.f), a);
+      s = make_float2(e.x > 1.f ? na.x : ea.x, e.y > 1.f ? na.y : ea.y);
+    }
+  } else {
+    gate_of<IO, KIND, kS, kTiny>(g.x, a.x, s.x);
+    gate_of<IO, KIND, kS, kTiny>(g.y, a.y, s.y);
+  }
+}
+
+// ------------------------------------------------------------------------------ rings
+
+// A warp's tile of one tensor: TW tokens of a column of COLS channels, in shared memory row after row.  It is copied in
+// and out in pieces of G bytes, neighbouring lanes neighbouring pieces: 16 where every row starts at a multiple of
+// 16 bytes, else 4, and 2 for bf16 rows that start between two words.  Pieces behind token `end` or channel D are zeros.
+// A lane has two channels of a column of 64, or one of 32.
+template <typename IO, int G, int TW, int COLS>
+struct Tile {
+  static constexpr int kBytes = TW * COLS * int(sizeof(IO));
+  static constexpr int kPerRow = COLS * int(sizeof(IO)) / G;
+  static constexpr int kPieces = TW * kPerRow / 32;  // a lane's
+
+  // the row and first channel of a lane's piece j, as what the lane adds and what j adds
+  static __device__ __forceinline__ int lane_row(int lane) { return kPerRow < 32 ? lane / kPerRow : 0; }
+  static __device__ __forceinline__ int lane_channel(int lane) {
+    return (kPerRow < 32 ? lane % kPerRow : lane) * (G / int(sizeof(IO)));
+  }
+  static __device__ __forceinline__ constexpr int piece_row(int j) { return 32 * j / kPerRow; }
+  static __device__ __forceinline__ constexpr int piece_channel(int j) {
+    return kPerRow > 32 ? 32 * j % kPerRow * (G / int(sizeof(IO))) : 0;
+  }
+  static __device__ __forceinline__ void copy(uint32_t dst, const IO* from, int bytes) {
+    if constexpr (G == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(bytes) : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(from), "r"(bytes) : "memory");
+  }
+
+  // src: the column's first channel in token 0 of this batch; left: channels of the column inside the tensor
+  static __device__ __forceinline__ void in(char* tile, const IO* src, int64_t stride, int64_t t0, int64_t end, int left,
+                                            int lane) {
+    if constexpr (G == 2) {  // IO is bf16
+      constexpr int kBatch = 8, kEach = COLS / 32;  // tokens whose values are on their way at once, channels of a lane
+      const int ch = kEach * lane;
+#pragma unroll
+      for (int i0 = 0; i0 < TW; i0 += kBatch) {
+        uint32_t r[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const uint16_t* row = reinterpret_cast<const uint16_t*>(src) + (t0 + i0 + i) * stride + ch;
+          const bool in = t0 + i0 + i < end;
+          r[i] = in && ch < left ? __ldg(row) : 0;
+          if (kEach == 2 && in && ch + 1 < left) r[i] |= uint32_t(__ldg(row + 1)) << 16;
+        }
+        using lane_t = std::conditional_t<kEach == 2, uint32_t, uint16_t>;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+          reinterpret_cast<lane_t*>(tile)[(i0 + i) * 32 + lane] = static_cast<lane_t>(r[i]);
+      }
+    } else if (t0 + TW <= end && left == COLS) {  // nothing to leave out
+      const uint32_t dst = smem_u32(tile) + lane * G;
+      const IO* from = src + (t0 + lane_row(lane)) * stride + lane_channel(lane);
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) copy(dst + 32 * j * G, from + piece_row(j) * stride + piece_channel(j), G);
+    } else {
+      const uint32_t dst = smem_u32(tile) + lane * G;
+#pragma unroll
+      for (int j = 0; j < kPieces; ++j) {
+        const int row = lane_row(lane) + piece_row(j), ch = lane_channel(lane) + piece_channel(j);
+        const bool ok = t0 + row < end && ch < left;
+        copy(dst + 32 * j * G, src + (ok ? (t0 + row) * stride + ch : 0), ok ? G : 0);
+      }
+    }
+  }
+
+  static __device__ __forceinline__ void out(const char* tile, IO* dst, int64_t stride, int64_t t0, int64_t end, int left,
+                                             int lane) {
+    using piece = std::conditional_t<G == 16, uint4, std::conditional_t<G == 4, uint32_t, uint16_t>>;
+    const char* from = tile + lane * G;
+    IO* to = dst + (t0 + lane_row(lane)) * stride + lane_channel(lane);
+    const bool whole = t0 + TW <= end && left == COLS;
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      if (whole || (t0 + lane_row(lane) + piece_row(j) < end && lane_channel(lane) + piece_channel(j) < left))
+        *reinterpret_cast<piece*>(to + piece_row(j) * stride + piece_channel(j)) =
+            *reinterpret_cast<const piece*>(from + 32 * j * G);
+    }
+  }
+};
+
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ------------------------------------------------------------------------------ chains
+
+// Hands values on from warp to warp: the giver writes them and arrives, the taker waits and reads; barrier `id` is the
+// taker's, used by nothing else.
+__device__ __forceinline__ void named_bar_arrive(uint32_t id, uint32_t nthreads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
+}
+__device__ __forceinline__ void give(int id) { asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void take(int id) { asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory"); }
+
+// ------------------------------------------------------------------------------ cluster
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+// An arrival that publishes nothing: it does not wait for the stores to global memory that are still on their way.
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// The address of this CTA's shared variable in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void st_peer(uint32_t addr, float2 v) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.x), "f"(v.y) : "memory");
+}
+
+constexpr int kCols = 64;  // channels of a cluster's column
+
+// Composes the maps of a CTA's warps, the first token's warp first (kBack: last), and writes the product P and the end
+// value into this CTA's place in every CTA of the cluster.  warp_map: P, then the forward value, or at 2 the adjoint's.
+template <bool kBack, int NW, int kParts>
+__device__ __forceinline__ void publish_map(float2 (*cta_map)[2][32], const float2 (&warp_map)[NW][kParts][32],
+                                            int rank, int K, int lane) {
+  float2 P = make_float2(1.f, 1.f), H = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int i = 0; i < NW; ++i) {
+    const int k = kBack ? NW - 1 - i : i;
+    const float2 kp = warp_map[k][0][lane];
+    H = fma_f32x2(kp, H, warp_map[k][kBack ? 2 : 1][lane]);
+    P = mul_f32x2(P, kp);
+  }
+  const uint32_t at = smem_u32(&cta_map[rank][0][lane]);
+  for (int k = 0; k < K; ++k) {
+    st_peer(peer_addr(at, k), P);
+    st_peer(peer_addr(at + sizeof(float2) * 32, k), H);
+  }
+}
+
+// ------------------------------------------------------------------------------ segments
+
+// The affine maps of whole segments, in the workspace: P and H (or R) of each (segment, batch), columns padded.
+struct Maps {
+  float* p;
+  int64_t padded;  // channels of all columns
+  __device__ __forceinline__ float* at(int64_t seg, int64_t batches, int64_t b, int part, int64_t c) const {
+    return p + ((seg * batches + b) * 2 + part) * padded + c;
+  }
+  __device__ __forceinline__ float2* pair_at(int64_t seg, int64_t batches, int64_t b, int part, int64_t c) const {
+    return reinterpret_cast<float2*>(at(seg, batches, b, part, c));
+  }
+};
+
+// ------------------------------------------------------------------------------ host
+
+// How a problem is shared among CTAs: `columns` of the kernel's width, each a cluster of CTAs over the sequence, which
+// walks it in `steps` steps, or `segments` CTAs with seg_len tokens each.
+struct Plan {
+  int64_t columns, seg_len;
+  int cluster, steps, segments;
+  Args args(const GatedProblem& p) const { return Args{p.L, p.D, p.sx, p.sg, seg_len, cluster, steps, segments}; }
+};
+
+inline int64_t columns64(const GatedProblem& p) { return (p.D + kCols - 1) / kCols; }
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// A cluster plan: as many CTAs along the sequence as fill the SMs once, `resident` on each.
+inline Plan cluster_plan(const GatedProblem& p, int64_t tile, int resident) {
+  const int64_t columns = columns64(p), tiles = ceil_div(p.L, tile);
+  int64_t K = int64_t(resident) * kSMs / (columns * p.b);
+  K = K < tiles / 2 ? K : tiles / 2;
+  K = K < 1 ? 1 : K > kMaxCluster ? kMaxCluster : K;
+  return Plan{columns, p.L, int(K), int(ceil_div(tiles, K)), 1};
+}
+
+// A plan with about `want` segments, whole multiples of `unit` tokens, walked in tiles.
+inline Plan segment_plan(const GatedProblem& p, int64_t columns, int64_t unit, int64_t want, int64_t tile) {
+  const int64_t units = ceil_div(p.L, unit), run = ceil_div(units, want < 1 ? 1 : want);
+  return Plan{columns, run * unit, 1, int(run * unit / tile), int(ceil_div(units, run))};
+}
+
+// Workspace of the segments' maps
+inline size_t maps_bytes(const GatedProblem& p, const Plan& plan) {
+  return plan.segments > 1 ? size_t(plan.segments) * size_t(p.b) * 2 * size_t(columns64(p)) * kCols * 4 : 0;
+}
+
+// The largest piece that every row of the tensors can be copied in.
+int piece_bytes(const GatedProblem& p, const void* x, const void* gate);
+
+// Launches kern on a grid of (columns x cluster, batch, segments), clusters along x.
+template <typename... KArgs, typename... Args_>
+cudaError_t launch(void (*kern)(KArgs...), const Plan& plan, int64_t batch, int threads, size_t smem, cudaStream_t st,
+                   Args_... args) {
+  cudaError_t e = cudaSuccess;
+  if (smem > 16 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(plan.columns * plan.cluster), static_cast<unsigned>(batch),
+                     static_cast<unsigned>(plan.segments));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = plan.cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = plan.cluster > 1 ? 2 : 1;
+  e = cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Calls f(io, piece, kind, complement) with the problem's types and constants.
+template <typename F>
+cudaError_t with_types(const GatedProblem& p, int piece, F f) {
+  auto by_comp = [&](auto io, auto g, auto kind) {
+    return p.complement ? f(io, g, kind, std::true_type()) : f(io, g, kind, std::false_type());
+  };
+  auto by_kind = [&](auto io, auto g) {
+    if (p.kind == SSD_GATE_DECAY) return by_comp(io, g, std::integral_constant<int, SSD_GATE_DECAY>());
+    if (p.kind == SSD_GATE_LOG) return by_comp(io, g, std::integral_constant<int, SSD_GATE_LOG>());
+    return by_comp(io, g, std::integral_constant<int, SSD_GATE_LOGIT>());
+  };
+  if (piece == 16)
+    return p.io_bf16 ? by_kind(uint16_t(), std::integral_constant<int, 16>())
+                     : by_kind(float(), std::integral_constant<int, 16>());
+  if (piece == 4)
+    return p.io_bf16 ? by_kind(uint16_t(), std::integral_constant<int, 4>())
+                     : by_kind(float(), std::integral_constant<int, 4>());
+  return by_kind(uint16_t(), std::integral_constant<int, 2>());
+}
+
+}  // namespace gated
+}  // namespace ssd

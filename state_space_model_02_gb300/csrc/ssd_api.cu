@@ -708,8 +708,19 @@ ssd_status need_ws(size_t need_bytes, const void* ws, size_t ws_bytes, const cha
 
 }  // namespace
 
+size_t ssd_gated_workspace_bytes(const ssd_gated_shape* shape) {
+  ssd::GatedProblem p;
+  return make_gated(shape, &p) == SSD_OK ? ssd::gated_workspace_bytes(p) : 0;
+}
+
+size_t ssd_gated_bwd_workspace_bytes(const ssd_gated_shape* shape) {
+  ssd::GatedProblem p;
+  return make_gated(shape, &p) == SSD_OK ? ssd::gated_bwd_workspace_bytes(p) : 0;
+}
+
 ssd_status ssd_gated_scan(const ssd_gated_shape* shape, const void* x, const void* gate, const float* init_state,
-                          void* y, float* final_state, float* states, void* stream) {
+                          void* y, float* final_state, float* states, void* workspace, size_t workspace_bytes,
+                          void* stream) {
   ssd::GatedProblem p;
   SSD_TRY(make_gated(shape, &p));
   SSD_TRY(need_elem(x, p.io_bf16, "x"));
@@ -718,7 +729,8 @@ ssd_status ssd_gated_scan(const ssd_gated_shape* shape, const void* x, const voi
   SSD_TRY(maybe(init_state, "init_state"));
   SSD_TRY(maybe(final_state, "final_state"));
   SSD_TRY(maybe(states, "states"));
-  SSD_TRY(cuda_ok(ssd::launch_gated_scan(p, x, gate, init_state, y, final_state, states,
+  SSD_TRY(need_ws(ssd::gated_workspace_bytes(p), workspace, workspace_bytes, "ssd_gated_workspace_bytes"));
+  SSD_TRY(cuda_ok(ssd::launch_gated_scan(p, x, gate, init_state, y, final_state, states, workspace,
                                          static_cast<cudaStream_t>(stream)),
                   "gated scan launch"));
   g_last_error[0] = '\0';
@@ -727,7 +739,7 @@ ssd_status ssd_gated_scan(const ssd_gated_shape* shape, const void* x, const voi
 
 ssd_status ssd_gated_scan_bwd(const ssd_gated_shape* shape, const void* x, const void* gate, const void* dy,
                               const float* states, const float* dfinal, void* dx, void* dgate, float* dinit,
-                              void* stream) {
+                              void* workspace, size_t workspace_bytes, void* stream) {
   ssd::GatedProblem p;
   SSD_TRY(make_gated(shape, &p));
   SSD_TRY(need_elem(x, p.io_bf16, "x"));
@@ -738,7 +750,8 @@ ssd_status ssd_gated_scan_bwd(const ssd_gated_shape* shape, const void* x, const
   SSD_TRY(need(dgate, "dgate"));
   SSD_TRY(maybe(dfinal, "dfinal"));
   SSD_TRY(maybe(dinit, "dinit"));
-  SSD_TRY(cuda_ok(ssd::launch_gated_scan_bwd(p, x, gate, dy, states, dfinal, dx, dgate, dinit,
+  SSD_TRY(need_ws(ssd::gated_bwd_workspace_bytes(p), workspace, workspace_bytes, "ssd_gated_bwd_workspace_bytes"));
+  SSD_TRY(cuda_ok(ssd::launch_gated_scan_bwd(p, x, gate, dy, states, dfinal, dx, dgate, dinit, workspace,
                                              static_cast<cudaStream_t>(stream)),
                   "gated scan backward launch"));
   g_last_error[0] = '\0';

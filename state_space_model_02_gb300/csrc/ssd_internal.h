@@ -141,11 +141,13 @@ cudaError_t launch_selective_scan(const SelProblem& p, const void* x, const void
 
 // Gated linear recurrence (gated_scan.cu): the scan, its backward pass, and a short run of tokens on a
 // resident state (new_state may be state).
+size_t gated_workspace_bytes(const GatedProblem& p);
+size_t gated_bwd_workspace_bytes(const GatedProblem& p);
 cudaError_t launch_gated_scan(const GatedProblem& p, const void* x, const void* gate, const float* init, void* y,
-                              float* final_state, float* states, cudaStream_t st);
+                              float* final_state, float* states, void* ws, cudaStream_t st);
 cudaError_t launch_gated_scan_bwd(const GatedProblem& p, const void* x, const void* gate, const void* dy,
                                   const float* states, const float* dfinal, void* dx, void* dgate, float* dinit,
-                                  cudaStream_t st);
+                                  void* ws, cudaStream_t st);
 cudaError_t launch_gated_decode(const GatedProblem& p, const void* x, const void* gate, const float* state,
                                 float* new_state, void* y, cudaStream_t st);
 

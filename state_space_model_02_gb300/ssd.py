@@ -30,7 +30,8 @@ EXPORTS = ("ssd_workspace_bytes", "ssd_get_workspace_layout", "ssd_fwd", "ssd_ch
            "ssd_chunk_state", "ssd_state_passing", "ssd_fwd_pass_state", "ssd_chunk_scan", "ssd_read_status",
            "ssd_selftest_wait_timeout", "ssd_fwd_noalloc", "ssd_decode", "ssd_selective_scan",
            "ssd_bwd_workspace_bytes", "ssd_bwd",
-           "ssd_gated_scan", "ssd_gated_scan_bwd", "ssd_gated_decode",
+           "ssd_gated_workspace_bytes", "ssd_gated_scan", "ssd_gated_bwd_workspace_bytes", "ssd_gated_scan_bwd",
+           "ssd_gated_decode",
            "ssd_norm_workspace_bytes", "ssd_group_norm", "ssd_norm_bwd_workspace_bytes", "ssd_group_norm_bwd",
            "ssd_status_str", "ssd_last_error", "ssd_kernel_plan")
 
@@ -99,8 +100,10 @@ def load_library(path: str = LIB_PATH):
         "ssd_selective_scan": ([ctypes.POINTER(SelShape)] + [vp] * 10, ctypes.c_int),
         "ssd_bwd_workspace_bytes": ([sp], ctypes.c_size_t),
         "ssd_bwd": ([sp] + [vp] * 17 + [ctypes.c_size_t, vp], ctypes.c_int),
-        "ssd_gated_scan": ([ctypes.POINTER(GatedShape)] + [vp] * 7, ctypes.c_int),
-        "ssd_gated_scan_bwd": ([ctypes.POINTER(GatedShape)] + [vp] * 9, ctypes.c_int),
+        "ssd_gated_workspace_bytes": ([ctypes.POINTER(GatedShape)], ctypes.c_size_t),
+        "ssd_gated_scan": ([ctypes.POINTER(GatedShape)] + [vp] * 7 + [ctypes.c_size_t, vp], ctypes.c_int),
+        "ssd_gated_bwd_workspace_bytes": ([ctypes.POINTER(GatedShape)], ctypes.c_size_t),
+        "ssd_gated_scan_bwd": ([ctypes.POINTER(GatedShape)] + [vp] * 9 + [ctypes.c_size_t, vp], ctypes.c_int),
         "ssd_gated_decode": ([ctypes.POINTER(GatedShape)] + [vp] * 6, ctypes.c_int),
         "ssd_norm_workspace_bytes": ([ctypes.POINTER(NormShape)], ctypes.c_size_t),
         "ssd_group_norm": ([ctypes.POINTER(NormShape)] + [vp] * 8 + [ctypes.c_size_t, vp], ctypes.c_int),
@@ -421,8 +424,12 @@ def gated_scan(x, gate, init_state=None, *, kind="logit", complement=False, y=No
     b, L, D = x.shape
     ctx, st = _on(x, stream)
     _dense(init_state, "init_state", x, torch.float32, (b, D))
-    states = None
+    lib = load_library()
+    nbytes = lib.ssd_gated_workspace_bytes(ctypes.byref(shape))
+    states = ws = None
     with ctx:
+        if nbytes:
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
         if y is None:
             y = torch.empty((b, L, D), dtype=x.dtype, device=x.device)
         if final_state is None and want_final:
@@ -431,8 +438,8 @@ def gated_scan(x, gate, init_state=None, *, kind="logit", complement=False, y=No
             states = torch.empty((b, -(-L // GATED_BLOCK), D), dtype=torch.float32, device=x.device)
     _dense(y, "y", x, x.dtype, x.shape)
     _dense(final_state, "final_state", x, torch.float32, (b, D))
-    _check(load_library().ssd_gated_scan(ctypes.byref(shape), _p(x), _p(gate), _p(init_state), _p(y),
-                                         _p(final_state), _p(states), st))
+    _check(lib.ssd_gated_scan(ctypes.byref(shape), _p(x), _p(gate), _p(init_state), _p(y), _p(final_state), _p(states),
+                              _p(ws), nbytes, st))
     return (y, final_state, states) if want_states else (y, final_state)
 
 
@@ -446,12 +453,17 @@ def gated_scan_bwd(x, gate, dy, states, dfinal=None, *, kind="logit", complement
     _dense(dy, "dy", x, x.dtype, x.shape)
     _dense(states, "states", x, torch.float32, (b, -(-L // GATED_BLOCK), D))
     _dense(dfinal, "dfinal", x, torch.float32, (b, D))
+    lib = load_library()
+    nbytes = lib.ssd_gated_bwd_workspace_bytes(ctypes.byref(shape))
+    ws = None
     with ctx:
         dx = torch.empty((b, L, D), dtype=x.dtype, device=x.device)
         dgate = torch.empty_like(dx)
         dinit = torch.empty((b, D), dtype=torch.float32, device=x.device)
-    _check(load_library().ssd_gated_scan_bwd(ctypes.byref(shape), _p(x), _p(gate), _p(dy), _p(states), _p(dfinal),
-                                             _p(dx), _p(dgate), _p(dinit), st))
+        if nbytes:
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    _check(lib.ssd_gated_scan_bwd(ctypes.byref(shape), _p(x), _p(gate), _p(dy), _p(states), _p(dfinal), _p(dx),
+                                  _p(dgate), _p(dinit), _p(ws), nbytes, st))
     return dict(dx=dx, dgate=dgate, dinit=dinit)
 
 

@@ -39,27 +39,41 @@ BAD_GATED = [(dict(batch=0), 1), (dict(seqlen=0), 1), (dict(dim=0), 1), (dict(io
 @pytest.mark.parametrize("bad,rc", BAD_GATED)
 def test_gated_shapes(lib, bad, rc):
     s = gated(**bad)
-    assert lib.ssd_gated_scan(s, *([GOOD] * 6), None) == rc and lib.ssd_last_error()
-    assert lib.ssd_gated_scan_bwd(s, *([GOOD] * 8), None) == rc
+    assert lib.ssd_gated_workspace_bytes(s) == 0 and lib.ssd_gated_bwd_workspace_bytes(s) == 0
+    assert lib.ssd_gated_scan(s, *([GOOD] * 7), 1 << 40, None) == rc and lib.ssd_last_error()
+    assert lib.ssd_gated_scan_bwd(s, *([GOOD] * 9), 1 << 40, None) == rc
     assert lib.ssd_gated_decode(s, *([GOOD] * 5), None) == rc
 
 
 def test_gated_pointers(lib):
-    assert lib.ssd_gated_scan(None, *([GOOD] * 6), None) == 1
+    assert lib.ssd_gated_scan(None, *([GOOD] * 7), 1 << 40, None) == 1
     # which arguments are required, and which alignment each has
     for call, count, required, elem in ((lib.ssd_gated_scan, 6, (0, 1, 3), (0, 1)),
                                         (lib.ssd_gated_scan_bwd, 8, (0, 1, 2, 3, 5, 6), (0, 1)),
                                         (lib.ssd_gated_decode, 5, (0, 1, 2, 3, 4), (0, 1))):
+        rest = () if call is lib.ssd_gated_decode else (GOOD, 1 << 40)
         for k in range(count):
             args = [GOOD] * count
             if k in required:
                 args[k] = None
-                assert call(gated(), *args, None) == 1, (call.__name__, k)
+                assert call(gated(), *args, *rest, None) == 1, (call.__name__, k)
             args[k] = ODD if k in elem else OK_ELEM
-            assert call(gated(), *args, None) == 3, (call.__name__, k)
+            assert call(gated(), *args, *rest, None) == 3, (call.__name__, k)
             if k in elem:
                 args[k] = OK_ELEM
-                assert call(gated(io_dtype=ssd.SSD_F32), *args, None) == 3
+                assert call(gated(io_dtype=ssd.SSD_F32), *args, *rest, None) == 3
+
+
+def test_gated_workspace(lib):
+    s = gated(batch=1, seqlen=1 << 20)   # two columns: the sequence is cut into segments
+    for query, call, count in ((lib.ssd_gated_workspace_bytes, lib.ssd_gated_scan, 6),
+                               (lib.ssd_gated_bwd_workspace_bytes, lib.ssd_gated_scan_bwd, 8)):
+        n = query(s)
+        assert n > 0
+        assert call(s, *([GOOD] * count), None, n, None) == 6 and b"workspace" in lib.ssd_last_error()
+        assert call(s, *([GOOD] * count), GOOD, n - 1, None) == 6
+        assert call(s, *([GOOD] * count), ctypes.c_void_p(0x100010), n, None) == 3
+    assert lib.ssd_gated_workspace_bytes(gated(batch=8, seqlen=8192, dim=5120)) == 0
 
 
 BAD_NORM = [(dict(batch=0), 1), (dict(seqlen=0), 1), (dict(channels=0), 1), (dict(ngroups=0), 1), (dict(ngroups=5), 1),
