@@ -1,197 +1,454 @@
-// group_norm -- group norm with an activation or a gate, channels last, and its backward pass.
+// group_norm -- group norm with an activation or a gate, channels last.
 //
-// One CTA takes the values of one (batch, group): seqlen positions of channels / ngroups neighbouring
-// channels.  It walks them once for the mean, once for the sum of squares around it, and once to write.
-#include "ptx.cuh"
-#include "ssd.h"
-#include "ssd_internal.h"
+// Bound by HBM: with bf16 each value is two bytes in and two out (and two of the gate), against about ten
+// operations.  Two shapes of the problem, two ways through it:
+//
+//   row_kernel    one position a statistic (the norm of single tokens): a group is a run of neighbouring channels, and
+//                 as many lanes or warps as hold it in registers read it once, reduce, and write.
+//   stat_kernel, apply_kernel   a group spans positions: CTAs take tiles of positions and channels; the first kernel leaves each
+//                 tile's mean and sum of squares around it, the second merges a group's tiles (with many of them a
+//                 kernel between the two does) and writes.  It takes the tiles from the last one back: what the
+//                 first kernel read last is still in the L2 cache.  (4 x 65536 x 256, bf16: 76 us; in batches of samples that
+//                 fit in the cache 102 us, the launches cost more than the second reading.)
+#include "group_norm.cuh"
+#include <atomic>
 
 namespace ssd {
+namespace norm {
 namespace {
 
-constexpr int kThreads = 256;
+// ------------------------------------------------------------------------------ rows
 
-__device__ __forceinline__ float ld_io(const float* p) { return __ldg(p); }
-__device__ __forceinline__ float ld_io(const uint16_t* p) { return __uint_as_float(uint32_t(__ldg(p)) << 16); }
-__device__ __forceinline__ void st_io(float* p, float v) { *p = v; }
-__device__ __forceinline__ void st_io(uint16_t* p, float v) { *p = static_cast<uint16_t>(pack_bf16x2(v, 0.f)); }
-
-__device__ __forceinline__ float sigmoid(float v) { return 1.f / (1.f + expf(-v)); }
-// d silu(v) / dv with s = sigmoid(v)
-__device__ __forceinline__ float silu_slope(float v, float s) { return s * (1.f + v * (1.f - s)); }
-
-__device__ float block_sum(float v) {
-  __shared__ float part[kThreads / 32];
+// A team of LANES lanes (0: of all the CTA's threads) holds a group's values in registers, R packs a thread.  Lanes keep
+// their group, with its weight and bias, and walk the samples, `stride` apart.  Every thread copies its own packs of the next
+// samples to shared memory ahead of use: loads on their way cost no registers, and no barrier stands between a
+// copy and its use.  A CTA takes one sample and leaves shared memory to the L1 cache, which serves weight and bias.
+template <typename IO, int VEC, int ACT, int R, int LANES>
+__global__ void __launch_bounds__(LANES ? 256 : 512, LANES ? 1 : 2) row_kernel(const NormProblem p, int stride, const IO* __restrict__ x,
+                                                                const IO* __restrict__ z, const float* __restrict__ w,
+                                                                const float* __restrict__ bias, IO* __restrict__ y,
+                                                                float* __restrict__ mean, float* __restrict__ rstd) {
+  constexpr bool kGated = ACT == SSD_NORM_GATE || ACT == SSD_NORM_GATE_FIRST;
+  constexpr int kTensors = kGated ? 2 : 1, kSlots = kRowSlots;
+  constexpr bool kRing = LANES != 0;  // with copies ahead; weight and bias stay in registers
+  using P = Pack<IO, VEC>;
+  extern __shared__ __align__(16) char ring[];
+  __shared__ float part[2][2][32];
+  const int threads = blockDim.x, lanes = LANES ? LANES : threads, l = LANES ? threadIdx.x % LANES : threadIdx.x;
+  typename P::raw* slots = reinterpret_cast<typename P::raw*>(ring) + threadIdx.x;
+  const int Cg = static_cast<int>(p.C / p.G);
+  const uint32_t team = LANES ? blockIdx.x * (threads / LANES) + threadIdx.x / LANES : blockIdx.x, groups = p.G;
+  const int64_t g = team % groups, first = team / groups;
+  const int64_t c0 = g * Cg + l * VEC;
+  const bool some = first < stride;  // the last teams may have no samples of their own
+  bool mine[R];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
-  __syncthreads();
-  v = 0.f;
+  for (int k = 0; k < R; ++k) mine[k] = some && (l + k * lanes) * VEC < Cg;
+  const float inv = 1.f / float(Cg);
+  const IO* xp = x + first * p.sx + c0;
+  const IO* zp = kGated ? z + first * p.sz + c0 : nullptr;
+  Vals<VEC> wv[kRing ? R : 1], bv[kRing ? R : 1];
+  if constexpr (kRing) {
 #pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) v += part[i];
-  return v;
-}
-
-template <typename IO>
-__global__ void norm_kernel(NormProblem p, const IO* __restrict__ x, const IO* __restrict__ z,
-                            const float* __restrict__ w, const float* __restrict__ bias, IO* __restrict__ y,
-                            float* __restrict__ mean, float* __restrict__ rstd) {
-  const int64_t n = blockIdx.x / p.G, g = blockIdx.x % p.G, Cg = p.C / p.G, count = p.S * Cg;
-  auto value = [&](int64_t i) {
-    const int64_t row = n * p.S + i / Cg, c = g * Cg + i % Cg;
-    float v = ld_io(x + row * p.sx + c);
-    if (p.act == SSD_NORM_GATE_FIRST) {
-      const float zv = ld_io(z + row * p.sz + c);
-      v *= zv * sigmoid(zv);
+    for (int k = 0; k < R; ++k) {
+      if (mine[k]) {
+        wv[k] = load_param<VEC>(w, c0 + k * lanes * VEC, 1.f);
+        bv[k] = load_param<VEC>(bias, c0 + k * lanes * VEC, 0.f);
+      }
     }
-    return v;
+  }
+  grid_dep_wait();
+  auto fetch = [&](int slot, int64_t n) {
+    typename P::raw* to = slots + slot * (R * kTensors) * threads;
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      if (mine[k] && n < p.n) {
+        P::copy(to + k * kTensors * threads, xp + k * lanes * VEC);
+        if constexpr (kGated) P::copy(to + (k * kTensors + 1) * threads, zp + k * lanes * VEC);
+      }
+    }
+    copies_commit();
+    xp += stride * p.sx;
+    if constexpr (kGated) zp += stride * p.sz;
   };
-  float mu = 0.f;
+  if constexpr (kRing) {
+#pragma unroll
+    for (int i = 0; i < kSlots; ++i) fetch(i, first + i * stride);
+  }
+  int slot = 0, odd = 0;
+  // all teams make the same number of rounds, the last of which may be empty for some
+  for (int64_t n = first; n - first < p.n; n += stride, odd ^= 1) {
+    P xr[R], zr[kGated ? R : 1];
+    if constexpr (kRing) {
+      copies_wait<kSlots - 1>();
+      const typename P::raw* at = slots + slot * (R * kTensors) * threads;
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        xr[k].r = at[k * kTensors * threads];
+        if constexpr (kGated) zr[k].r = at[(k * kTensors + 1) * threads];
+      }
+      fetch(slot, n + kSlots * stride);
+      slot = slot + 1 == kSlots ? 0 : slot + 1;
+    } else {
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        if (mine[k]) {
+          xr[k].load(xp + k * lanes * VEC);
+          if constexpr (kGated) zr[k].load(zp + k * lanes * VEC);
+        }
+      }
+    }
+    Vals<VEC> v[R], acc = splat<VEC>(0.f);
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      v[k] = splat<VEC>(0.f);
+      if (mine[k]) {
+        v[k] = xr[k].widen();
+        if constexpr (ACT == SSD_NORM_GATE_FIRST) v[k] = v[k] * silu<IO>(zr[k].widen());
+      }
+      if (!p.rms) acc = acc + v[k];
+    }
+    float mu = 0.f;
+    if (!p.rms) {
+      mu = team_sum<LANES>(sum_of(acc), part[odd][0]) * inv;
+#pragma unroll
+      for (int k = 0; k < R; ++k)
+        if (mine[k]) v[k] = v[k] - mu;
+    }
+    acc = v[0] * v[0];
+#pragma unroll
+    for (int k = 1; k < R; ++k) acc = fma(v[k], v[k], acc);
+    const float r = rsqrtf(team_sum<LANES>(sum_of(acc), part[odd][1]) * inv + p.eps);
+    if (n < p.n) {
+      IO* yp = y + n * p.C + c0;
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        if (mine[k]) {
+          if constexpr (kRing) {
+            v[k] = fma(v[k] * r, wv[k], bv[k]);
+          } else {
+            const int64_t c = c0 + k * lanes * VEC;
+            v[k] = fma(v[k] * r, load_param<VEC>(w, c, 1.f), load_param<VEC>(bias, c, 0.f));
+          }
+          if constexpr (ACT == SSD_NORM_SILU) v[k] = silu<IO>(v[k]);
+          if constexpr (ACT == SSD_NORM_GATE) v[k] = v[k] * silu<IO>(zr[k].widen());
+          P out;
+          out.narrow(v[k]);
+          out.store(yp + k * lanes * VEC);
+        }
+      }
+      if (some && l == 0) {
+        if (mean) mean[n * p.G + g] = mu;
+        if (rstd) rstd[n * p.G + g] = r;
+      }
+    }
+    if constexpr (!kRing) break;
+  }
+  grid_dep_launch();
+}
+
+// Packs of a group that a CTA of 512 threads holds
+constexpr int kMostPacks = 2048;
+bool rows_ok(const NormProblem& p, int vec) { return p.S == 1 && p.C / p.G / vec <= kMostPacks; }
+
+template <typename IO, int VEC, int ACT, int R, int LANES>
+cudaError_t launch_rows(const NormProblem& p, int threads, const IO* x, const IO* z, const float* w, const float* b, IO* y,
+                        float* mean, float* rstd, cudaStream_t st) {
+  auto kern = row_kernel<IO, VEC, ACT, R, LANES>;
+  int64_t stride = p.n, per_cta = 1;
+  size_t smem = 0;
+  if constexpr (LANES != 0) {
+    smem = size_t(threads) * R * (ACT == SSD_NORM_GATE || ACT == SSD_NORM_GATE_FIRST ? 2 : 1) * kRowSlots * Pack<IO, VEC>::kBytes;
+    static std::atomic<int> known{0};  // CTAs that an SM holds; 0: not asked for yet
+    int resident = known.load(std::memory_order_relaxed);
+    if (resident == 0) {
+      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+      if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kern, threads, smem);
+      if (e != cudaSuccess) return e;
+      resident = resident < 1 ? 1 : resident;
+      known.store(resident, std::memory_order_relaxed);
+    }
+    // teams: a multiple of the groups, as many as the SMs hold at once, and no more than there are rows to take
+    per_cta = threads / LANES;
+    const int64_t fit = int64_t(kSMs) * resident * per_cta / p.G;
+    stride = fit < 1 ? 1 : fit < p.n ? fit : p.n;
+  }
+  return launch_pdl(kern, dim3(static_cast<unsigned>(ceil_div(stride * p.G, per_cta))), dim3(threads), smem, st, p,
+                    static_cast<int>(stride), x, z, w, b, y, mean, rstd);
+}
+
+template <typename IO, int VEC, int ACT>
+cudaError_t rows(const NormProblem& p, const IO* x, const IO* z, const float* w, const float* b, IO* y, float* mean,
+                 float* rstd, cudaStream_t st) {
+  const int64_t items = p.C / p.G / VEC;
+  // with few rows the time is one row's latency: a CTA a group, one pack a thread as far as that goes
+  if (items > 32 && items <= 1024 && p.n * p.G <= 2 * kSMs) {
+    if (items <= 512) return launch_rows<IO, VEC, ACT, 1, 0>(p, round_up(items, 32), x, z, w, b, y, mean, rstd, st);
+    return launch_rows<IO, VEC, ACT, 2, 0>(p, round_up(ceil_div(items, 2), 32), x, z, w, b, y, mean, rstd, st);
+  }
+  if (items <= 8) return launch_rows<IO, VEC, ACT, 1, 8>(p, 256, x, z, w, b, y, mean, rstd, st);
+  if (items <= 32) return launch_rows<IO, VEC, ACT, 1, 32>(p, 256, x, z, w, b, y, mean, rstd, st);
+  if (items <= 64) return launch_rows<IO, VEC, ACT, 2, 32>(p, 256, x, z, w, b, y, mean, rstd, st);
+  if (items <= 96) return launch_rows<IO, VEC, ACT, 3, 32>(p, 256, x, z, w, b, y, mean, rstd, st);
+  if (items <= 256) return launch_rows<IO, VEC, ACT, 2, 0>(p, round_up(ceil_div(items, 2), 32), x, z, w, b, y, mean, rstd, st);
+  return launch_rows<IO, VEC, ACT, 4, 0>(p, round_up(ceil_div(items, 4), 32), x, z, w, b, y, mean, rstd, st);
+}
+
+// ------------------------------------------------------------------------------ tiles
+
+// The statistics of each tile: parts[(n G + g) parts + part].  Every thread sums its channels around their value in
+// its first position, so that a mean far from zero costs no bits; the threads of a group then merge.
+template <typename IO, int VEC, int ACT>
+__global__ void __launch_bounds__(kTileThreads) stat_kernel(const NormProblem p, const Cut k, const IO* __restrict__ x,
+                                                            const IO* __restrict__ z, float2* __restrict__ parts) {
+  constexpr bool kFirst = ACT == SSD_NORM_GATE_FIRST;
+  constexpr int kGo = kFirst ? kAhead / 2 : kAhead;
+  __shared__ Stat all[kTileThreads];
+  const Place q = place_of<false>(p, k, VEC);
+  grid_dep_wait();
+  Vals<VEC> at = splat<VEC>(0.f), s = at, ss = at;
+  int count = 0;
+  if (q.live && q.row0 + q.deep < q.row1) {
+    count = static_cast<int>((q.row1 - q.row0 - q.deep - 1) / k.depth) + 1;  // positions of this thread
+    const IO* xp = x + (q.n * p.S + q.row0 + q.deep) * p.sx + q.c0;
+    const IO* zp = kFirst ? z + (q.n * p.S + q.row0 + q.deep) * p.sz + q.c0 : nullptr;
+    const int64_t dx = k.depth * p.sx, dz = k.depth * p.sz;
+    auto value = [&](const Pack<IO, VEC>& xr, const Pack<IO, VEC>& zr) {
+      return kFirst ? xr.widen() * silu<IO>(zr.widen()) : xr.widen();
+    };
+    auto add = [&](const Pack<IO, VEC>& xr, const Pack<IO, VEC>& zr) {
+      const Vals<VEC> d = value(xr, zr) - at;
+      s = s + d;
+      ss = fma(d, d, ss);
+    };
+    Pack<IO, VEC> xr[kGo], zr[kFirst ? kGo : 1];
+    if (!p.rms) {
+      xr[0].load(xp);
+      if constexpr (kFirst) zr[0].load(zp);
+      at = value(xr[0], zr[0]);
+    }
+    for (int i = 0; i < count; i += kGo) {
+#pragma unroll
+      for (int j = 0; j < kGo; ++j) {  // past the last position the last one again
+        const int64_t at = i + j < count ? j : count - 1 - i;
+        xr[j].load(xp + at * dx);
+        if constexpr (kFirst) zr[j].load(zp + at * dz);
+      }
+      xp += kGo * dx;
+      if constexpr (kFirst) zp += kGo * dz;
+#pragma unroll
+      for (int j = 0; j < kGo; ++j)
+        if (i + j < count) add(xr[j], zr[kFirst ? j : 0]);
+    }
+  }
+  Stat t{float(count * VEC), 0.f, 0.f};
+  if (p.rms) {  // the sum of squares around zero, as `m2`
+    t.m2 = sum_of(ss);
+  } else if (count > 0) {
+    const float n = float(count), inv = 1.f / n;
+    const Vals<VEC> m = fma(s, splat<VEC>(inv), at);
+    t.mean = sum_of(m) * (1.f / VEC);
+    const Vals<VEC> d = m - t.mean;
+    t.m2 = fmaxf(sum_of(ss) - sum_of(s * s) * inv, 0.f) + n * sum_of(d * d);
+  }
+  all[threadIdx.x] = t;
+  __syncthreads();
+  // some lanes a group: its packs, in each of the positions taken at once
+  const int width = k.subs == 1 ? k.per_group : k.items, entries = width * k.depth;
+  int lanes = 1;
+  while (lanes < 32 && lanes < entries) lanes *= 2;
+  const int l = threadIdx.x % lanes, teams = kTileThreads / lanes;
+  const float total = float((q.row1 - q.row0) * (k.subs == 1 ? width : min(width, k.per_group - q.sub * k.items)) * VEC);
+  for (int g0 = 0; g0 < q.groups; g0 += teams) {
+    const int g = g0 + threadIdx.x / lanes;
+    float mean = 0.f, m2 = 0.f;
+    if (!p.rms) {
+      if (g < q.groups)
+        for (int i = l; i < entries; i += lanes) {
+          const Stat& b = all[i / width * k.items + g * width + i % width];
+          mean = fmaf(b.n, b.mean, mean);
+        }
+      mean = lanes_sum(mean, lanes) / total;
+    }
+    if (g < q.groups)
+      for (int i = l; i < entries; i += lanes) {
+        const Stat& b = all[i / width * k.items + g * width + i % width];
+        const float d = b.mean - mean;
+        m2 += p.rms ? b.m2 : fmaf(b.n * d, d, b.m2);
+      }
+    m2 = lanes_sum(m2, lanes);
+    if (l == 0 && g < q.groups)
+      parts[(q.n * p.G + q.g0 + g) * k.parts() + q.sub * k.chunks + q.chunk] = make_float2(mean, m2);
+  }
+  grid_dep_launch();
+}
+
+// Mean and rstd of group `id` of this launch's samples from its tiles, in each of the `lanes` neighbouring lanes (a power
+// of two) that share its tiles.
+__device__ __forceinline__ float2 merge_parts(const NormProblem& p, const Cut& k, const float2* parts, int64_t id, int vec,
+                                              int lanes) {
+  const int lane = threadIdx.x % lanes, count = k.parts();
+  const float2* of = parts + id * count;
+  auto size = [&](uint32_t i) {  // values of a tile
+    const uint32_t chunk = i % uint32_t(k.chunks);
+    const int first = static_cast<int>(i / uint32_t(k.chunks)) * k.items;
+    const int64_t rows = p.S - chunk * k.rows < k.rows ? p.S - chunk * k.rows : k.rows;
+    return float(rows) * float(k.subs == 1 ? k.per_group : min(k.items, k.per_group - first)) * float(vec);
+  };
+  const float total = float(p.S) * float(p.C / p.G);
+  constexpr int kHeld = 8;  // a lane's first tiles, whose loads are on their way at once
+  float2 held[kHeld];
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j) held[j] = lane + lanes * j < count ? of[lane + lanes * j] : make_float2(0.f, 0.f);
+  float mean = 0.f, m2 = 0.f;
   if (!p.rms) {
-    for (int64_t i = threadIdx.x; i < count; i += kThreads) mu += value(i);
-    mu = block_sum(mu) / float(count);
+#pragma unroll
+    for (int j = 0; j < kHeld; ++j)
+      if (lane + lanes * j < count) mean = fmaf(size(lane + lanes * j), held[j].x, mean);
+    for (int i = lane + lanes * kHeld; i < count; i += lanes) mean = fmaf(size(i), of[i].x, mean);
+    mean = lanes_sum(mean, lanes) / total;
   }
-  float sq = 0.f;
-  for (int64_t i = threadIdx.x; i < count; i += kThreads) {
-    const float v = value(i) - mu;
-    sq = fmaf(v, v, sq);
-  }
-  const float r = 1.f / sqrtf(block_sum(sq) / float(count) + p.eps);
-  for (int64_t i = threadIdx.x; i < count; i += kThreads) {
-    const int64_t row = n * p.S + i / Cg, c = g * Cg + i % Cg;
-    float v = fmaf((value(i) - mu) * r, w ? w[c] : 1.f, bias ? bias[c] : 0.f);
-    if (p.act == SSD_NORM_SILU) v *= sigmoid(v);
-    if (p.act == SSD_NORM_GATE) {
-      const float zv = ld_io(z + row * p.sz + c);
-      v *= zv * sigmoid(zv);
-    }
-    st_io(y + row * p.C + c, v);
-  }
-  if (threadIdx.x == 0) {
-    if (mean) mean[blockIdx.x] = mu;
-    if (rstd) rstd[blockIdx.x] = r;
+  auto add = [&](int i, float2 t) {
+    const float d = t.x - mean;
+    m2 += p.rms ? t.y : fmaf(size(i) * d, d, t.y);
+  };
+#pragma unroll
+  for (int j = 0; j < kHeld; ++j)
+    if (lane + lanes * j < count) add(lane + lanes * j, held[j]);
+  for (int i = lane + lanes * kHeld; i < count; i += lanes) add(i, of[i]);
+  return make_float2(mean, rsqrtf(lanes_sum(m2, lanes) / total + p.eps));
+}
+
+// One warp a group: stats[n G + g] from many tiles.
+__global__ void __launch_bounds__(128) merge_kernel(const NormProblem p, const Cut k, int vec, const float2* __restrict__ parts,
+                                                    float2* __restrict__ stats) {
+  const int64_t id = int64_t(blockIdx.x) * 4 + threadIdx.x / 32;
+  grid_dep_launch();
+  grid_dep_wait();
+  if (id < p.n * p.G) {
+    const float2 s = merge_parts(p, k, parts, id, vec, 32);
+    if (threadIdx.x % 32 == 0) stats[id] = s;
   }
 }
 
-// The gradient of one value's n, and what its dx and dz need.
-struct Back {
-  float dn, xhat, gate, slope, v, p;  // gate = silu(z), slope = silu'(z), v = x as read, p = n
-};
-
-template <typename IO>
-__device__ __forceinline__ Back back_of(const NormProblem& p, int64_t row, int64_t c, const IO* x, const IO* z,
-                                        const float* w, const float* bias, const IO* dy, float mu, float r) {
-  Back k{};
-  k.v = ld_io(x + row * p.sx + c);
-  float v = k.v;
-  if (z) {
-    const float zv = ld_io(z + row * p.sz + c), s = sigmoid(zv);
-    k.gate = zv * s;
-    k.slope = silu_slope(zv, s);
-    if (p.act == SSD_NORM_GATE_FIRST) v *= k.gate;
+// Writes y from the statistics: merged ones, or (stats null) the tiles' own.
+template <typename IO, int VEC, int ACT>
+__global__ void __launch_bounds__(kTileThreads) apply_kernel(const NormProblem p, const Cut k, const IO* __restrict__ x,
+                                                             const IO* __restrict__ z, const float* __restrict__ w,
+                                                             const float* __restrict__ bias, IO* __restrict__ y,
+                                                             float* __restrict__ mean, float* __restrict__ rstd,
+                                                             const float2* __restrict__ parts,
+                                                             const float2* __restrict__ stats) {
+  constexpr bool kGated = ACT == SSD_NORM_GATE || ACT == SSD_NORM_GATE_FIRST;
+  __shared__ float2 of_group[kTileThreads];
+  const Place q = place_of<true>(p, k, VEC);
+  Vals<VEC> wv, bv;
+  if (q.live) {
+    wv = load_param<VEC>(w, q.c0, 1.f);
+    bv = load_param<VEC>(bias, q.c0, 0.f);
   }
-  k.xhat = (v - mu) * r;
-  k.p = fmaf(k.xhat, w ? w[c] : 1.f, bias ? bias[c] : 0.f);
-  k.dn = ld_io(dy + row * p.C + c);
-  if (p.act == SSD_NORM_SILU) k.dn *= silu_slope(k.p, sigmoid(k.p));
-  return k;
-}
-
-template <typename IO>
-__global__ void norm_bwd_kernel(NormProblem p, const IO* __restrict__ x, const IO* __restrict__ z,
-                                const float* __restrict__ w, const float* __restrict__ bias,
-                                const IO* __restrict__ dy, const float* __restrict__ mean,
-                                const float* __restrict__ rstd, IO* __restrict__ dx, IO* __restrict__ dz) {
-  const int64_t n = blockIdx.x / p.G, g = blockIdx.x % p.G, Cg = p.C / p.G, count = p.S * Cg;
-  const float mu = mean ? mean[blockIdx.x] : 0.f, r = rstd[blockIdx.x];
-  float m1 = 0.f, m2 = 0.f;
-  for (int64_t i = threadIdx.x; i < count; i += kThreads) {
-    const int64_t row = n * p.S + i / Cg, c = g * Cg + i % Cg;
-    const Back k = back_of(p, row, c, x, z, w, bias, dy, mu, r);
-    const float q = k.dn * (p.act == SSD_NORM_GATE ? k.gate : 1.f) * (w ? w[c] : 1.f);
-    m1 += q;
-    m2 = fmaf(q, k.xhat, m2);
-  }
-  m1 = p.rms ? 0.f : block_sum(m1) / float(count);
-  m2 = block_sum(m2) / float(count);
-  for (int64_t i = threadIdx.x; i < count; i += kThreads) {
-    const int64_t row = n * p.S + i / Cg, c = g * Cg + i % Cg;
-    const Back k = back_of(p, row, c, x, z, w, bias, dy, mu, r);
-    const float q = k.dn * (p.act == SSD_NORM_GATE ? k.gate : 1.f) * (w ? w[c] : 1.f);
-    float dv = r * (q - m1 - k.xhat * m2);
-    if (p.act == SSD_NORM_GATE) st_io(dz + row * p.C + c, k.dn * k.p * k.slope);
-    if (p.act == SSD_NORM_GATE_FIRST) {
-      st_io(dz + row * p.C + c, dv * k.v * k.slope);
-      dv *= k.gate;
-    }
-    st_io(dx + row * p.C + c, dv);
-  }
-}
-
-// dweight and dbias: one thread a channel, over all rows
-template <typename IO>
-__global__ void norm_param_kernel(NormProblem p, const IO* __restrict__ x, const IO* __restrict__ z,
-                                  const float* __restrict__ w, const float* __restrict__ bias,
-                                  const IO* __restrict__ dy, const float* __restrict__ mean,
-                                  const float* __restrict__ rstd, float* __restrict__ dw, float* __restrict__ db) {
-  const int64_t c = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (c >= p.C) return;
-  const int64_t g = c / (p.C / p.G);
-  float sw = 0.f, sb = 0.f;
-  for (int64_t n = 0; n < p.n; ++n) {
-    const float mu = mean ? mean[n * p.G + g] : 0.f, r = rstd[n * p.G + g];
-    for (int64_t s = 0; s < p.S; ++s) {
-      const Back k = back_of(p, n * p.S + s, c, x, z, w, bias, dy, mu, r);
-      const float dn = k.dn * (p.act == SSD_NORM_GATE ? k.gate : 1.f);
-      sw = fmaf(dn, k.xhat, sw);
-      sb += dn;
+  grid_dep_wait();
+  int lanes = 32;  // of a group: all of the slab's at once
+  while (lanes * q.groups > kTileThreads) lanes /= 2;
+  const int g = threadIdx.x / lanes;
+  {
+    const int64_t id = q.n * p.G + q.g0 + (g < q.groups ? g : 0);
+    const float2 s = stats ? stats[id] : merge_parts(p, k, parts, id, VEC, lanes);
+    if (threadIdx.x % lanes == 0 && g < q.groups) {
+      of_group[g] = s;
+      if (q.chunk == 0 && q.sub == 0) {
+        if (mean) mean[id] = s.x;
+        if (rstd) rstd[id] = s.y;
+      }
     }
   }
-  if (dw) dw[c] = sw;
-  if (db) db[c] = sb;
+  __syncthreads();
+  if (q.live && q.row0 + q.deep < q.row1) {
+    const float2 s = of_group[k.subs == 1 ? uint32_t(q.col) / uint32_t(k.per_group) : 0];
+    wv = wv * s.y;
+    const int count = static_cast<int>((q.row1 - q.row0 - q.deep - 1) / k.depth) + 1;
+    const int64_t row = q.n * p.S + q.row0 + q.deep, dx = k.depth * p.sx, dz = k.depth * p.sz, dy = k.depth * p.C;
+    const IO* xp = x + row * p.sx + q.c0;
+    const IO* zp = kGated ? z + row * p.sz + q.c0 : nullptr;
+    IO* yp = y + row * p.C + q.c0;
+    constexpr int kGo = kGated ? kAhead / 2 : kAhead;
+    Pack<IO, VEC> xr[kGo], zr[kGated ? kGo : 1];
+    auto write = [&](IO* to, const Pack<IO, VEC>& xr, const Pack<IO, VEC>& zr) {
+      Vals<VEC> v = xr.widen();
+      if constexpr (ACT == SSD_NORM_GATE_FIRST) v = v * silu<IO>(zr.widen());
+      v = fma(v - s.x, wv, bv);
+      if constexpr (ACT == SSD_NORM_SILU) v = silu<IO>(v);
+      if constexpr (ACT == SSD_NORM_GATE) v = v * silu<IO>(zr.widen());
+      Pack<IO, VEC> out;
+      out.narrow(v);
+      out.store(to);
+    };
+    for (int i = 0; i < count; i += kGo) {
+#pragma unroll
+      for (int j = 0; j < kGo; ++j) {
+        const int64_t at = i + j < count ? j : count - 1 - i;
+        xr[j].load(xp + at * dx);
+        if constexpr (kGated) zr[j].load(zp + at * dz);
+      }
+#pragma unroll
+      for (int j = 0; j < kGo; ++j)
+        if (i + j < count) write(yp + j * dy, xr[j], zr[kGated ? j : 0]);
+      xp += kGo * dx;
+      if constexpr (kGated) zp += kGo * dz;
+      yp += kGo * dy;
+    }
+  }
+  grid_dep_launch();
+}
+
+// Tiles of a group that every CTA of the second kernel merges by itself (a few loads a lane); more go through
+// merge_kernel.
+constexpr int kMergeInPlace = 96;
+
+size_t tile_bytes(const NormProblem& p, int vec) {
+  const size_t groups = size_t(p.n) * size_t(p.G);
+  return align_up(groups * size_t(cut_of(p, vec).parts()) * sizeof(float2), 256) + align_up(groups * sizeof(float2), 256);
 }
 
 }  // namespace
+}  // namespace norm
 
-size_t norm_workspace_bytes(const NormProblem&) { return 0; }
-size_t norm_bwd_workspace_bytes(const NormProblem&) { return 0; }
+size_t norm_workspace_bytes(const NormProblem& p) {
+  size_t most = 0;
+  for (int vec = 1; vec <= (p.io_bf16 ? 8 : 4); vec *= 2) {  // whatever the tensors' alignment allows
+    if ((p.C / p.G) % vec != 0 || norm::rows_ok(p, vec)) continue;
+    const size_t b = norm::tile_bytes(p, vec);
+    most = b > most ? b : most;
+  }
+  return most;
+}
 
 cudaError_t launch_group_norm(const NormProblem& p, const void* x, const void* z, const float* w, const float* b,
                               void* y, float* mean, float* rstd, void* ws, cudaStream_t st) {
-  const unsigned grid = static_cast<unsigned>(p.n * p.G);
-  if (p.io_bf16)
-    norm_kernel<uint16_t><<<grid, kThreads, 0, st>>>(p, static_cast<const uint16_t*>(x),
-                                                     static_cast<const uint16_t*>(z), w, b,
-                                                     static_cast<uint16_t*>(y), mean, rstd);
-  else
-    norm_kernel<float><<<grid, kThreads, 0, st>>>(p, static_cast<const float*>(x), static_cast<const float*>(z), w, b,
-                                                  static_cast<float*>(y), mean, rstd);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_group_norm_bwd(const NormProblem& p, const void* x, const void* z, const float* w,
-                                  const float* b, const void* dy, const float* mean, const float* rstd, void* dx,
-                                  void* dz, float* dw, float* db, void* ws, cudaStream_t st) {
-  const unsigned grid = static_cast<unsigned>(p.n * p.G), cols = static_cast<unsigned>((p.C + 63) / 64);
-  if (p.io_bf16) {
-    using T = uint16_t;
-    norm_bwd_kernel<T><<<grid, kThreads, 0, st>>>(p, static_cast<const T*>(x), static_cast<const T*>(z), w, b,
-                                                  static_cast<const T*>(dy), mean, rstd, static_cast<T*>(dx),
-                                                  static_cast<T*>(dz));
-    if (dw || db)
-      norm_param_kernel<T><<<cols, 64, 0, st>>>(p, static_cast<const T*>(x), static_cast<const T*>(z), w, b,
-                                                static_cast<const T*>(dy), mean, rstd, dw, db);
-  } else {
-    using T = float;
-    norm_bwd_kernel<T><<<grid, kThreads, 0, st>>>(p, static_cast<const T*>(x), static_cast<const T*>(z), w, b,
-                                                  static_cast<const T*>(dy), mean, rstd, static_cast<T*>(dx),
-                                                  static_cast<T*>(dz));
-    if (dw || db)
-      norm_param_kernel<T><<<cols, 64, 0, st>>>(p, static_cast<const T*>(x), static_cast<const T*>(z), w, b,
-                                                static_cast<const T*>(dy), mean, rstd, dw, db);
-  }
-  return cudaGetLastError();
+  using namespace norm;
+  const int vec = pack_width(p, x, z);
+  return with_types(p, vec, [&](auto io, auto v, auto act) -> cudaError_t {
+    using IO = decltype(io);
+    constexpr int VEC = decltype(v)::value, ACT = decltype(act)::value;
+    const IO* xi = static_cast<const IO*>(x);
+    const IO* zi = static_cast<const IO*>(z);
+    IO* yo = static_cast<IO*>(y);
+    if (rows_ok(p, VEC)) return rows<IO, VEC, ACT>(p, xi, zi, w, b, yo, mean, rstd, st);
+    const Cut k = cut_of(p, VEC);
+    const dim3 grid(static_cast<unsigned>(p.n * k.chunks * k.slabs));
+    const int64_t groups = p.n * p.G;
+    float2* parts = static_cast<float2*>(ws);
+    float2* stats = nullptr;
+    cudaError_t e = launch_pdl(stat_kernel<IO, VEC, ACT>, grid, dim3(kTileThreads), 0, st, p, k, xi, zi, parts);
+    if (e == cudaSuccess && k.parts() > kMergeInPlace) {
+      stats = parts + align_up(size_t(groups) * size_t(k.parts()) * sizeof(float2), 256) / sizeof(float2);
+      e = launch_pdl(merge_kernel, dim3(static_cast<unsigned>(ceil_div(groups, 4))), dim3(128), 0, st, p, k, VEC,
+                     static_cast<const float2*>(parts), stats);
+    }
+    if (e != cudaSuccess) return e;
+    return launch_pdl(apply_kernel<IO, VEC, ACT>, grid, dim3(kTileThreads), 0, st, p, k, xi, zi, w, b, yo, mean, rstd,
+                      static_cast<const float2*>(parts), static_cast<const float2*>(stats));
+  });
 }
 
 }  // namespace ssd

@@ -1,0 +1,363 @@
+// group_norm.cuh -- what the group norm's forward and backward kernels share: packs of neighbouring channels, the
+// activation, merging of statistics, and how a problem is cut into CTAs.
+#pragma once
+#include <type_traits>
+
+#include "ptx.cuh"
+#include "ssd.h"
+#include "ssd_internal.h"
+
+namespace ssd {
+namespace norm {
+
+// ------------------------------------------------------------------------------ values
+
+// VEC neighbouring channels of one position as float32: pairs, which the packed instructions take, or one value
+template <int VEC>
+struct Vals {
+  static constexpr int kN = VEC == 1 ? 1 : VEC / 2;
+  using T = std::conditional_t<VEC == 1, float, float2>;
+  T v[kN];
+};
+__device__ __forceinline__ float bc(float f, float) { return f; }
+__device__ __forceinline__ float2 bc(float f, float2) { return make_float2(f, f); }
+__device__ __forceinline__ float mul1(float a, float b) { return a * b; }
+__device__ __forceinline__ float2 mul1(float2 a, float2 b) { return mul_f32x2(a, b); }
+__device__ __forceinline__ float fma1(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ float2 fma1(float2 a, float2 b, float2 c) { return fma_f32x2(a, b, c); }
+__device__ __forceinline__ float both(float a) { return a; }
+__device__ __forceinline__ float both(float2 a) { return a.x + a.y; }
+template <typename F>
+__device__ __forceinline__ float map1(float a, F f) { return f(a); }
+template <typename F>
+__device__ __forceinline__ float2 map1(float2 a, F f) { return make_float2(f(a.x), f(a.y)); }
+
+template <int VEC>
+__device__ __forceinline__ Vals<VEC> splat(float f) {
+  Vals<VEC> r;
+#pragma unroll
+  for (int i = 0; i < r.kN; ++i) r.v[i] = bc(f, r.v[i]);
+  return r;
+}
+template <int VEC>
+__device__ __forceinline__ Vals<VEC> operator*(const Vals<VEC>& a, const Vals<VEC>& b) {
+  Vals<VEC> r;
+#pragma unroll
+  for (int i = 0; i < r.kN; ++i) r.v[i] = mul1(a.v[i], b.v[i]);
+  return r;
+}
+template <int VEC>
+__device__ __forceinline__ Vals<VEC> operator*(const Vals<VEC>& a, float b) {
+  Vals<VEC> r;
+#pragma unroll
+  for (int i = 0; i < r.kN; ++i) r.v[i] = mul1(a.v[i], bc(b, a.v[i]));
+  return r;
+}
+template <int VEC>  // a b + c
+__device__ __forceinline__ Vals<VEC> fma(const Vals<VEC>& a, const Vals<VEC>& b, const Vals<VEC>& c) {
+  Vals<VEC> r;
+#pragma unroll
+  for (int i = 0; i < r.kN; ++i) r.v[i] = fma1(a.v[i], b.v[i], c.v[i]);
+  return r;
+}
+template <int VEC>
+__device__ __forceinline__ Vals<VEC> operator+(const Vals<VEC>& a, const Vals<VEC>& b) {
+  return fma(a, splat<VEC>(1.f), b);
+}
+template <int VEC>
+__device__ __forceinline__ Vals<VEC> operator-(const Vals<VEC>& a, const Vals<VEC>& b) {
+  return fma(b, splat<VEC>(-1.f), a);
+}
+template <int VEC>
+__device__ __forceinline__ Vals<VEC> operator-(const Vals<VEC>& a, float b) {
+  return fma(splat<VEC>(b), splat<VEC>(-1.f), a);
+}
+template <int VEC>
+__device__ __forceinline__ float sum_of(const Vals<VEC>& a) {
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < a.kN; ++i) s += both(a.v[i]);
+  return s;
+}
+template <int VEC, typename F>
+__device__ __forceinline__ Vals<VEC> map(const Vals<VEC>& a, F f) {
+  Vals<VEC> r;
+#pragma unroll
+  for (int i = 0; i < r.kN; ++i) r.v[i] = map1(a.v[i], f);
+  return r;
+}
+
+// The same as they lie in memory
+template <typename IO, int VEC>
+struct Pack {
+  static constexpr int kBytes = VEC * int(sizeof(IO));
+  using raw = std::conditional_t<kBytes == 16, uint4, std::conditional_t<kBytes == 8, uint2, std::conditional_t<kBytes == 4, uint32_t, uint16_t>>>;
+  raw r;
+
+  __device__ __forceinline__ void load(const IO* p) { r = __ldg(reinterpret_cast<const raw*>(p)); }
+  // An asynchronous copy of a pack to shared memory (of single bf16 values, which it does not take, a plain one).
+  static __device__ __forceinline__ void copy(raw* to, const IO* from) {
+    if constexpr (kBytes == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+    else if constexpr (kBytes == 8)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+    else if constexpr (kBytes == 4)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+    else
+      *to = __ldg(reinterpret_cast<const raw*>(from));
+  }
+  __device__ __forceinline__ void store(IO* p) const { *reinterpret_cast<raw*>(p) = r; }
+  __device__ __forceinline__ Vals<VEC> widen() const {
+    Vals<VEC> f;
+    if constexpr (kBytes == 16 && sizeof(IO) == 2) {
+      f.v[0] = make_float2(bf16lo_to_f32(r.x), bf16hi_to_f32(r.x));
+      f.v[1] = make_float2(bf16lo_to_f32(r.y), bf16hi_to_f32(r.y));
+      f.v[2] = make_float2(bf16lo_to_f32(r.z), bf16hi_to_f32(r.z));
+      f.v[3] = make_float2(bf16lo_to_f32(r.w), bf16hi_to_f32(r.w));
+    } else if constexpr (kBytes == 16) {
+      f.v[0] = make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
+      f.v[1] = make_float2(__uint_as_float(r.z), __uint_as_float(r.w));
+    } else if constexpr (kBytes == 8) {
+      f.v[0] = make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
+    } else if constexpr (VEC == 2) {
+      f.v[0] = make_float2(bf16lo_to_f32(r), bf16hi_to_f32(r));
+    } else if constexpr (sizeof(IO) == 4) {
+      f.v[0] = __uint_as_float(r);
+    } else {
+      f.v[0] = __uint_as_float(uint32_t(r) << 16);
+    }
+    return f;
+  }
+  __device__ __forceinline__ void narrow(const Vals<VEC>& f) {
+    if constexpr (kBytes == 16 && sizeof(IO) == 2)
+      r = make_uint4(pack_bf16x2(f.v[0].x, f.v[0].y), pack_bf16x2(f.v[1].x, f.v[1].y), pack_bf16x2(f.v[2].x, f.v[2].y),
+                     pack_bf16x2(f.v[3].x, f.v[3].y));
+    else if constexpr (kBytes == 16)
+      r = make_uint4(__float_as_uint(f.v[0].x), __float_as_uint(f.v[0].y), __float_as_uint(f.v[1].x), __float_as_uint(f.v[1].y));
+    else if constexpr (kBytes == 8)
+      r = make_uint2(__float_as_uint(f.v[0].x), __float_as_uint(f.v[0].y));
+    else if constexpr (VEC == 2)
+      r = pack_bf16x2(f.v[0].x, f.v[0].y);
+    else if constexpr (sizeof(IO) == 4)
+      r = __float_as_uint(f.v[0]);
+    else
+      r = static_cast<uint16_t>(pack_bf16x2(f.v[0], 0.f));
+  }
+};
+
+// VEC float32 parameters from channel c on; `or_else` where there are none
+template <int VEC>
+__device__ __forceinline__ Vals<VEC> load_param(const float* p, int64_t c, float or_else) {
+  Vals<VEC> f;
+  if (!p) return splat<VEC>(or_else);
+  if constexpr (VEC % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < VEC / 4; ++i) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(p + c) + i);
+      f.v[2 * i] = make_float2(v.x, v.y);
+      f.v[2 * i + 1] = make_float2(v.z, v.w);
+    }
+  } else if constexpr (VEC == 2) {
+    f.v[0] = __ldg(reinterpret_cast<const float2*>(p + c));
+  } else {
+    f.v[0] = __ldg(p + c);
+  }
+  return f;
+}
+template <int VEC>
+__device__ __forceinline__ void store_param(float* p, int64_t c, const Vals<VEC>& f) {
+#pragma unroll
+  for (int i = 0; i < f.kN; ++i) *reinterpret_cast<typename Vals<VEC>::T*>(p + c + 2 * i) = f.v[i];
+}
+
+__device__ __forceinline__ float rcp_approx(float v) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+// 1 / (1 + exp(-v)), with the MUFU unit's reciprocal (one unit in the last place).  For bf16 results the exponential is
+// the MUFU unit's too, and below v = -87 the result is 0 (its value is under 2^-125).  Float32 results take expf of
+// -|v|, which stays in range.
+template <typename IO, int VEC>
+__device__ __forceinline__ Vals<VEC> sigmoid(const Vals<VEC>& v) {
+  if constexpr (sizeof(IO) == 2) {
+    const Vals<VEC> e = map(v * -1.44269502f, [](float f) { return ex2(f); });
+    return map(e + splat<VEC>(1.f), [](float f) { return rcp_approx(f); });
+  } else {
+    return map(v, [](float f) {
+      const float e = expf(-fabsf(f)), r = rcp_approx(1.f + e);
+      return f >= 0.f ? r : e * r;
+    });
+  }
+}
+template <typename IO, int VEC>
+__device__ __forceinline__ Vals<VEC> silu(const Vals<VEC>& v) {
+  return v * sigmoid<IO>(v);
+}
+// The slope of silu at v, from s = sigmoid(v): s (1 + v (1 - s))
+template <int VEC>
+__device__ __forceinline__ Vals<VEC> silu_slope(const Vals<VEC>& v, const Vals<VEC>& s) {
+  return s * fma(v, splat<VEC>(1.f) - s, splat<VEC>(1.f));
+}
+
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ------------------------------------------------------------------------------ statistics
+
+// Mean of `n` values and sum of squares around it.  Runs of values merge without loss, whatever their means are (sums of
+// squares around zero would lose the variance of values far from it):
+//     mean = sum n_i mean_i / sum n_i,   m2 = sum m2_i + n_i (mean_i - mean)^2
+struct Stat {
+  float n, mean, m2;
+};
+
+// The sum over `lanes` neighbouring lanes (a power of two), in all of them.
+__device__ __forceinline__ float lanes_sum(float v, int lanes) {
+  for (int o = lanes / 2; o; o /= 2) v += __shfl_xor_sync(~0u, v, o);
+  return v;
+}
+
+// The sum over the LANES neighbouring lanes of a group, or (LANES 0) over the CTA's threads.  part: the CTA's, another one for
+// every call that no barrier separates.
+template <int LANES>
+__device__ __forceinline__ float team_sum(float v, float* part) {
+#pragma unroll
+  for (int o = (LANES ? LANES : 32) / 2; o; o /= 2) v += __shfl_xor_sync(~0u, v, o);
+  if constexpr (LANES == 0) {
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = threadIdx.x % 32 < blockDim.x / 32 ? part[threadIdx.x % 32] : 0.f;
+#pragma unroll
+    for (int o = 16; o; o /= 2) v += __shfl_xor_sync(~0u, v, o);
+  }
+  return v;
+}
+
+constexpr int kRowSlots = 4;  // samples that a thread has on their way or at hand
+
+// ------------------------------------------------------------------------------ sharing
+
+// Channels in one load of a thread: 16 bytes of them where a group is a multiple of that and every row starts at a
+// multiple of 16 bytes, else two, else one.
+inline int pack_width(const NormProblem& p, const void* x, const void* z) {
+  const int e = p.io_bf16 ? 2 : 4;
+  const int64_t Cg = p.C / p.G;
+  for (int v = 16 / e; v > 1; v = v > 2 ? 2 : 1) {
+    const uintptr_t a = uintptr_t(v * e) - 1;
+    if (Cg % v == 0 && p.sx % v == 0 && (reinterpret_cast<uintptr_t>(x) & a) == 0 &&
+        (!z || (p.sz % v == 0 && (reinterpret_cast<uintptr_t>(z) & a) == 0)))
+      return v;
+  }
+  return 1;
+}
+
+// Calls f(io, vec, act) with the types and constants of the problem.
+template <typename F>
+cudaError_t with_types(const NormProblem& p, int vec, F f) {
+  auto by_act = [&](auto io, auto v) {
+    switch (p.act) {
+      case SSD_NORM_SILU: return f(io, v, std::integral_constant<int, SSD_NORM_SILU>());
+      case SSD_NORM_GATE: return f(io, v, std::integral_constant<int, SSD_NORM_GATE>());
+      case SSD_NORM_GATE_FIRST: return f(io, v, std::integral_constant<int, SSD_NORM_GATE_FIRST>());
+      default: return f(io, v, std::integral_constant<int, SSD_NORM_NONE>());
+    }
+  };
+  if (!p.io_bf16)
+    return vec == 4   ? by_act(float(), std::integral_constant<int, 4>())
+           : vec == 2 ? by_act(float(), std::integral_constant<int, 2>())
+                      : by_act(float(), std::integral_constant<int, 1>());
+  return vec == 8   ? by_act(uint16_t(), std::integral_constant<int, 8>())
+         : vec == 2 ? by_act(uint16_t(), std::integral_constant<int, 2>())
+                    : by_act(uint16_t(), std::integral_constant<int, 1>());
+}
+inline bool gated(const NormProblem& p) { return p.act == SSD_NORM_GATE || p.act == SSD_NORM_GATE_FIRST; }
+
+inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline int round_up(int64_t v, int64_t to) { return int(ceil_div(v, to) * to); }
+
+// Positions and channels cut into tiles of one CTA each.  Along the channels a slab of `items` packs: whole groups,
+// or one of the `subs` equal parts of a group that has more packs than a CTA has threads.  Along the positions
+// `chunks` runs of `rows`.
+constexpr int kTileThreads = 256;
+constexpr int kAhead = 8;  // positions whose loads a thread has on their way at once
+struct Cut {
+  int64_t rows;
+  int slabs, chunks;
+  int items;      // packs of a slab (the last one of a group's parts may have fewer)
+  int per_group;  // packs of a group
+  int groups;     // groups of a slab (the last slab may have fewer)
+  int subs;       // slabs of a group
+  int depth;      // positions that the CTA's threads take at once
+  __host__ __device__ int parts() const { return chunks * subs; }  // tiles that a group's statistics are merged from
+};
+inline Cut cut_of(const NormProblem& p, int vec) {
+  Cut k{};
+  const int64_t per = p.C / p.G / vec;
+  if (per <= kTileThreads) {
+    k.slabs = int(ceil_div(p.G, kTileThreads / per));
+    k.groups = int(ceil_div(p.G, k.slabs));
+    k.slabs = int(ceil_div(p.G, k.groups));
+    k.items = k.groups * int(per);
+    k.subs = 1;
+  } else {
+    k.groups = 1;
+    k.subs = int(ceil_div(per, kTileThreads));
+    k.items = int(ceil_div(per, k.subs));
+    k.slabs = int(p.G) * k.subs;
+  }
+  k.per_group = int(per);
+  k.depth = kTileThreads / k.items;
+  // CTAs enough for 64 KB of loads on their way in an SM; each takes whole rounds of kAhead positions.  (8 x 4096 x 512, bf16:
+  // 24.0 us with two CTAs an SM, 25.4 with three, 28.3 with four, 27.7 with one.)
+  const int bytes = vec * (p.io_bf16 ? 2 : 4), per_sm = bytes == 16 ? 2 : bytes == 8 ? 4 : 8;
+  const int64_t want = ceil_div(per_sm * kSMs, p.n * k.slabs), most = ceil_div(p.S, kAhead * k.depth);
+  const int64_t round = kAhead * k.depth;
+  k.rows = ceil_div(ceil_div(p.S, want < most ? want : most), round) * round;
+  k.chunks = int(ceil_div(p.S, k.rows));
+  return k;
+}
+
+// The tile of a CTA and the thread's place in it.  blockIdx.x counts slabs, then chunks, then samples.
+struct Place {
+  int64_t n, row0, row1, c0;  // c0: the thread's first channel
+  int slab, chunk;
+  int col, deep, g0, groups, sub;          // column of packs and position of the thread; groups of the slab
+  bool live;
+};
+// kBack: the tiles in the other order, so that what the kernel before read last, and the L2 cache still has, comes
+// first.
+template <bool kBack>
+__device__ __forceinline__ Place place_of(const NormProblem& p, const Cut& k, int vec) {
+  Place q;
+  const uint32_t at = kBack ? gridDim.x - 1 - blockIdx.x : blockIdx.x, slabs = k.slabs, chunks = k.chunks;  // 32-bit divisions
+  q.slab = at % slabs;
+  q.chunk = at / slabs % chunks;
+  q.n = at / slabs / chunks;
+  q.row0 = q.chunk * k.rows;
+  q.row1 = q.row0 + k.rows < p.S ? q.row0 + k.rows : p.S;
+  const uint32_t items = k.items;
+  q.col = threadIdx.x % items;
+  q.deep = threadIdx.x / items;
+  if (k.subs == 1) {
+    q.g0 = q.slab * k.groups;
+    q.groups = p.G - q.g0 < k.groups ? static_cast<int>(p.G - q.g0) : k.groups;
+    q.sub = 0;
+    q.live = q.deep < k.depth && q.col < q.groups * k.per_group;
+    q.c0 = (int64_t(q.g0) * k.per_group + q.col) * vec;
+  } else {
+    q.g0 = q.slab / k.subs;
+    q.groups = 1;
+    q.sub = q.slab % k.subs;
+    const int first = q.sub * k.items;
+    q.live = q.deep < k.depth && first + q.col < k.per_group;
+    q.c0 = (int64_t(q.g0) * k.per_group + first + q.col) * vec;
+  }
+  return q;
+}
+
+}  // namespace norm
+}  // namespace ssd

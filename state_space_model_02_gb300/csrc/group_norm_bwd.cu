@@ -1,0 +1,483 @@
+// group_norm_bwd -- backward pass of the group norm.
+//
+// With dn the gradient of n = w xhat + b, q = w dn, and means over a group's values,
+//     dv = rstd (q - mean(q) - xhat mean(q xhat)),   dw = sum dn xhat,   db = sum dn.
+// Bound by HBM: x and dy (and z) in, dx (and dz) out, six or ten bytes a value with bf16.  The same two ways as in
+// the forward pass:
+//
+//   row_bwd_kernel    one position a statistic: a team keeps its group and walks the samples, each read once, and keeps
+//                     its share of dw and db in registers.
+//   sum_kernel, dx_kernel   a group spans positions: per tile and channel the sums of dn and dn xhat, of which a group's means
+//                     are weighted sums; then dx from the second reading, the last tiles first.
+//
+// The shares of dw and db, one row each of [2][C] in the workspace, are added up in a fixed order by param_kernel.
+#include <atomic>
+
+#include "group_norm.cuh"
+
+namespace ssd {
+namespace norm {
+namespace {
+
+// One pack of values and what its gradients need
+template <typename IO, int VEC, int ACT>
+struct Back {
+  Vals<VEC> xhat, dn, gate, slope, n;  // gate = silu(z), slope = its derivative
+
+  __device__ __forceinline__ void from(const Pack<IO, VEC>& x, const Pack<IO, VEC>& z, const Pack<IO, VEC>& dy, float mu,
+                                       float r, const Vals<VEC>& w, const Vals<VEC>& b) {
+    Vals<VEC> v = x.widen();
+    if constexpr (ACT == SSD_NORM_GATE || ACT == SSD_NORM_GATE_FIRST) {
+      const Vals<VEC> zv = z.widen(), s = sigmoid<IO>(zv);
+      gate = zv * s;
+      slope = silu_slope(zv, s);
+      if constexpr (ACT == SSD_NORM_GATE_FIRST) v = v * gate;
+    }
+    xhat = (v - mu) * r;
+    dn = dy.widen();
+    if constexpr (ACT == SSD_NORM_SILU || ACT == SSD_NORM_GATE) n = fma(xhat, w, b);
+    if constexpr (ACT == SSD_NORM_SILU) dn = dn * silu_slope(n, sigmoid<IO>(n));
+    if constexpr (ACT == SSD_NORM_GATE) {
+      slope = dn * n * slope;  // dz
+      dn = dn * gate;
+    }
+  }
+};
+
+// ------------------------------------------------------------------------------ rows
+
+template <typename IO, int VEC, int ACT, int R, int LANES>
+__global__ void __launch_bounds__(LANES ? 256 : 512) row_bwd_kernel(
+    const NormProblem p, int stride, const IO* __restrict__ x, const IO* __restrict__ z, const float* __restrict__ w,
+    const float* __restrict__ bias, const IO* __restrict__ dy, const float* __restrict__ mean,
+    const float* __restrict__ rstd, IO* __restrict__ dx, IO* __restrict__ dz, float* __restrict__ shares) {
+  constexpr bool kGated = ACT == SSD_NORM_GATE || ACT == SSD_NORM_GATE_FIRST;
+  constexpr int kTensors = kGated ? 3 : 2, kSlots = kRowSlots;
+  using P = Pack<IO, VEC>;
+  extern __shared__ __align__(16) char ring[];
+  __shared__ float part[2][2][32];
+  const int threads = blockDim.x, lanes = LANES ? LANES : threads, l = LANES ? threadIdx.x % LANES : threadIdx.x;
+  typename P::raw* slots = reinterpret_cast<typename P::raw*>(ring) + threadIdx.x;
+  const int Cg = static_cast<int>(p.C / p.G);
+  const uint32_t team = LANES ? blockIdx.x * (threads / LANES) + threadIdx.x / LANES : blockIdx.x, groups = p.G;
+  const int64_t g = team % groups, first = team / groups;
+  const int64_t c0 = g * Cg + l * VEC;
+  const bool some = first < stride;  // the last teams may have no samples of their own
+  bool mine[R];
+#pragma unroll
+  for (int k = 0; k < R; ++k) mine[k] = some && (l + k * lanes) * VEC < Cg;
+  const float inv = 1.f / float(Cg);
+  const IO* xp = x + first * p.sx + c0;
+  const IO* zp = kGated ? z + first * p.sz + c0 : nullptr;
+  const IO* dp = dy + first * p.C + c0;
+  grid_dep_wait();
+  auto fetch = [&](int slot, int64_t n) {
+    typename P::raw* to = slots + slot * (R * kTensors) * threads;
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      if (mine[k] && n < p.n) {
+        P::copy(to + k * kTensors * threads, xp + k * lanes * VEC);
+        P::copy(to + (k * kTensors + 1) * threads, dp + k * lanes * VEC);
+        if constexpr (kGated) P::copy(to + (k * kTensors + 2) * threads, zp + k * lanes * VEC);
+      }
+    }
+    copies_commit();
+    xp += stride * p.sx;
+    dp += stride * p.C;
+    if constexpr (kGated) zp += stride * p.sz;
+  };
+#pragma unroll
+  for (int i = 0; i < kSlots; ++i) fetch(i, first + i * stride);
+  auto stat = [&](int64_t n) {
+    return some && n < p.n ? make_float2(mean ? mean[n * p.G + g] : 0.f, rstd[n * p.G + g]) : make_float2(0.f, 0.f);
+  };
+  float2 next = stat(first);
+  Vals<VEC> dw[R], db[R];
+#pragma unroll
+  for (int k = 0; k < R; ++k) dw[k] = db[k] = splat<VEC>(0.f);
+
+  int slot = 0, odd = 0;
+  // all teams make the same number of rounds, the last of which may be empty for some
+  for (int64_t n = first; n - first < p.n; n += stride, odd ^= 1) {
+    const float2 st = next;
+    next = stat(n + stride);
+    copies_wait<kSlots - 1>();
+    const typename P::raw* at = slots + slot * (R * kTensors) * threads;
+    Back<IO, VEC, ACT> v[R];
+    P xr[R];
+    float m1 = 0.f, m2 = 0.f;
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      if (mine[k] && n < p.n) {
+        const int64_t c = c0 + k * lanes * VEC;
+        const Vals<VEC> wv = load_param<VEC>(w, c, 1.f);
+        P dr, zr;
+        xr[k].r = at[k * kTensors * threads];
+        dr.r = at[(k * kTensors + 1) * threads];
+        if constexpr (kGated) zr.r = at[(k * kTensors + 2) * threads];
+        Vals<VEC> bv;
+        if constexpr (ACT == SSD_NORM_SILU || ACT == SSD_NORM_GATE) bv = load_param<VEC>(bias, c, 0.f);
+        v[k].from(xr[k], zr, dr, st.x, st.y, wv, bv);
+        dw[k] = fma(v[k].dn, v[k].xhat, dw[k]);
+        db[k] = db[k] + v[k].dn;
+        v[k].dn = v[k].dn * wv;
+        m1 += sum_of(v[k].dn);
+        m2 += sum_of(v[k].dn * v[k].xhat);
+      }
+    }
+    fetch(slot, n + kSlots * stride);
+    slot = slot + 1 == kSlots ? 0 : slot + 1;
+    m1 = p.rms ? 0.f : team_sum<LANES>(m1, part[odd][0]) * inv;
+    m2 = team_sum<LANES>(m2, part[odd][1]) * inv;
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      if (mine[k] && n < p.n) {
+        const int64_t to = n * p.C + c0 + k * lanes * VEC;
+        Vals<VEC> dv = ((v[k].dn - m1) - v[k].xhat * m2) * st.y;
+        P out;
+        if constexpr (ACT == SSD_NORM_GATE) {
+          out.narrow(v[k].slope);
+          out.store(dz + to);
+        }
+        if constexpr (ACT == SSD_NORM_GATE_FIRST) {
+          out.narrow(dv * xr[k].widen() * v[k].slope);
+          out.store(dz + to);
+          dv = dv * v[k].gate;
+        }
+        out.narrow(dv);
+        out.store(dx + to);
+      }
+    }
+  }
+  if (shares) {
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      if (mine[k]) {
+        float* row = shares + first * 2 * p.C;
+        store_param<VEC>(row, c0 + k * lanes * VEC, dw[k]);
+        store_param<VEC>(row, p.C + c0 + k * lanes * VEC, db[k]);
+      }
+    }
+  }
+  grid_dep_launch();
+}
+
+// Packs of a group that a CTA of 512 threads holds
+constexpr int kMostPacks = 1024;
+bool rows_ok(const NormProblem& p, int vec) { return p.S == 1 && p.C / p.G / vec <= kMostPacks; }
+
+// How the rows are shared: threads of a CTA, lanes of a team (0: all), packs of a thread and samples taken at once.
+struct RowPlan {
+  int threads, lanes, R;
+  int64_t stride;
+};
+RowPlan row_plan(const NormProblem& p, int vec) {
+  const int64_t items = p.C / p.G / vec;
+  RowPlan k{256, items <= 8 ? 8 : 32, items <= 32 ? 1 : 2, 0};
+  if (items > 64) k = RowPlan{round_up(items <= 512 ? items : ceil_div(items, 2), 32), 0, items <= 512 ? 1 : 2, 0};
+  // threads that an SM holds, by the registers of a pack or two; teams are a multiple of the groups
+  const int resident = k.R == 1 ? 512 : 512, per_sm = resident / k.threads < 1 ? 1 : resident / k.threads;
+  const int64_t fit = int64_t(kSMs) * per_sm * (k.lanes ? k.threads / k.lanes : 1) / p.G;
+  k.stride = fit < 1 ? 1 : fit < p.n ? fit : p.n;
+  return k;
+}
+
+template <typename IO, int VEC, int ACT, int R, int LANES>
+cudaError_t launch_rows(const NormProblem& p, const RowPlan& k, const IO* x, const IO* z, const float* w, const float* b,
+                        const IO* dy, const float* mean, const float* rstd, IO* dx, IO* dz, float* shares, cudaStream_t st) {
+  auto kern = row_bwd_kernel<IO, VEC, ACT, R, LANES>;
+  constexpr int kPerThread = R * (ACT == SSD_NORM_GATE || ACT == SSD_NORM_GATE_FIRST ? 3 : 2) * kRowSlots * Pack<IO, VEC>::kBytes;
+  static std::atomic<bool> known{false};
+  if (!known.load(std::memory_order_relaxed)) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 512 * kPerThread);
+    if (e != cudaSuccess) return e;
+    known.store(true, std::memory_order_relaxed);
+  }
+  const int64_t ctas = ceil_div(k.stride * p.G, LANES ? k.threads / LANES : 1);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(k.threads), size_t(k.threads) * kPerThread, st, p,
+                    static_cast<int>(k.stride), x, z, w, b, dy, mean, rstd, dx, dz, shares);
+}
+
+// ------------------------------------------------------------------------------ tiles
+
+// Per tile: its channels' sums of dn xhat and dn (a row of [2][C] of `shares` for each sample and chunk), and each group's
+// sums of q and q xhat.
+template <typename IO, int VEC, int ACT>
+__global__ void __launch_bounds__(kTileThreads) sum_kernel(const NormProblem p, const Cut k, const IO* __restrict__ x,
+                                                           const IO* __restrict__ z, const float* __restrict__ w,
+                                                           const float* __restrict__ bias, const IO* __restrict__ dy,
+                                                           const float* __restrict__ mean,
+                                                           const float* __restrict__ rstd, float2* __restrict__ parts,
+                                                           float* __restrict__ shares) {
+  constexpr bool kGated = ACT == SSD_NORM_GATE || ACT == SSD_NORM_GATE_FIRST;
+  constexpr int kGo = kAhead / 2;
+  __shared__ Vals<VEC> all[2][kTileThreads];
+  __shared__ float2 sums[kTileThreads];
+  const Place q = place_of<false>(p, k, VEC);
+  Vals<VEC> wv = splat<VEC>(0.f), bv = wv, sw = wv, sb = wv;
+  if (q.live) {
+    wv = load_param<VEC>(w, q.c0, 1.f);
+    bv = load_param<VEC>(bias, q.c0, 0.f);
+  }
+  grid_dep_wait();
+  if (q.live && q.row0 + q.deep < q.row1) {
+    const int64_t id = q.n * p.G + q.g0 + (k.subs == 1 ? uint32_t(q.col) / uint32_t(k.per_group) : 0);
+    const float mu = mean ? mean[id] : 0.f, r = rstd[id];
+    const int count = static_cast<int>((q.row1 - q.row0 - q.deep - 1) / k.depth) + 1;
+    const int64_t row = q.n * p.S + q.row0 + q.deep, ex = k.depth * p.sx, ez = k.depth * p.sz, ey = k.depth * p.C;
+    const IO* xp = x + row * p.sx + q.c0;
+    const IO* zp = kGated ? z + row * p.sz + q.c0 : nullptr;
+    const IO* dp = dy + row * p.C + q.c0;
+    for (int i = 0; i < count; i += kGo) {
+      Pack<IO, VEC> xr[kGo], dr[kGo], zr[kGated ? kGo : 1];
+#pragma unroll
+      for (int j = 0; j < kGo; ++j) {  // past the last position the last one again
+        const int64_t at = i + j < count ? j : count - 1 - i;
+        xr[j].load(xp + at * ex);
+        dr[j].load(dp + at * ey);
+        if constexpr (kGated) zr[j].load(zp + at * ez);
+      }
+      xp += kGo * ex;
+      dp += kGo * ey;
+      if constexpr (kGated) zp += kGo * ez;
+#pragma unroll
+      for (int j = 0; j < kGo; ++j) {
+        if (i + j < count) {
+          Back<IO, VEC, ACT> v;
+          v.from(xr[j], zr[kGated ? j : 0], dr[j], mu, r, wv, bv);
+          sw = fma(v.dn, v.xhat, sw);
+          sb = sb + v.dn;
+        }
+      }
+    }
+  }
+  all[0][threadIdx.x] = sw;
+  all[1][threadIdx.x] = sb;
+  __syncthreads();
+  if (q.deep == 0 && q.live) {  // the threads of the first position add the others'
+    for (int d = 1; d < k.depth; ++d) {
+      sw = sw + all[0][d * k.items + q.col];
+      sb = sb + all[1][d * k.items + q.col];
+    }
+    float* row = shares + (q.n * k.chunks + q.chunk) * 2 * p.C;
+    store_param<VEC>(row, q.c0, sw);
+    store_param<VEC>(row, p.C + q.c0, sb);
+  }
+  if (threadIdx.x < k.items)
+    sums[threadIdx.x] = q.live ? make_float2(sum_of(sb * wv), sum_of(sw * wv)) : make_float2(0.f, 0.f);
+  __syncthreads();
+  const int width = k.subs == 1 ? k.per_group : k.items;
+  int lanes = 1;
+  while (lanes < 32 && lanes < width) lanes *= 2;
+  const int l = threadIdx.x % lanes, teams = kTileThreads / lanes;
+  for (int g0 = 0; g0 < q.groups; g0 += teams) {
+    const int g = g0 + threadIdx.x / lanes;
+    float2 a = make_float2(0.f, 0.f);
+    if (g < q.groups)
+      for (int i = l; i < width; i += lanes) {
+        a.x += sums[g * width + i].x;
+        a.y += sums[g * width + i].y;
+      }
+    a.x = lanes_sum(a.x, lanes);
+    a.y = lanes_sum(a.y, lanes);
+    if (l == 0 && g < q.groups) parts[(q.n * p.G + q.g0 + g) * k.parts() + q.sub * k.chunks + q.chunk] = a;
+  }
+  grid_dep_launch();
+}
+
+// The means of q and q xhat of group `id` from its tiles, in each of `lanes` neighbouring lanes.
+__device__ __forceinline__ float2 add_parts(const NormProblem& p, const Cut& k, const float2* parts, int64_t id, int lanes) {
+  const int count = k.parts();
+  const float2* of = parts + id * count;
+  float2 a = make_float2(0.f, 0.f);
+#pragma unroll 8
+  for (int i = threadIdx.x % lanes; i < count; i += lanes) {
+    const float2 t = of[i];
+    a.x += t.x;
+    a.y += t.y;
+  }
+  const float inv = 1.f / (float(p.S) * float(p.C / p.G));
+  return make_float2(p.rms ? 0.f : lanes_sum(a.x, lanes) * inv, lanes_sum(a.y, lanes) * inv);
+}
+__global__ void __launch_bounds__(128) add_kernel(const NormProblem p, const Cut k, const float2* __restrict__ parts,
+                                                  float2* __restrict__ sums) {
+  const int64_t id = int64_t(blockIdx.x) * 4 + threadIdx.x / 32;
+  grid_dep_launch();
+  grid_dep_wait();
+  if (id < p.n * p.G) {
+    const float2 s = add_parts(p, k, parts, id, 32);
+    if (threadIdx.x % 32 == 0) sums[id] = s;
+  }
+}
+
+template <typename IO, int VEC, int ACT>
+__global__ void __launch_bounds__(kTileThreads) dx_kernel(const NormProblem p, const Cut k, const IO* __restrict__ x,
+                                                          const IO* __restrict__ z, const float* __restrict__ w,
+                                                          const float* __restrict__ bias, const IO* __restrict__ dy,
+                                                          const float* __restrict__ mean,
+                                                          const float* __restrict__ rstd, IO* __restrict__ dx,
+                                                          IO* __restrict__ dz, const float2* __restrict__ parts,
+                                                          const float2* __restrict__ merged) {
+  constexpr bool kGated = ACT == SSD_NORM_GATE || ACT == SSD_NORM_GATE_FIRST;
+  constexpr int kGo = kAhead / 2;
+  __shared__ float2 of_group[kTileThreads];
+  const Place q = place_of<true>(p, k, VEC);
+  Vals<VEC> wv, bv;
+  if (q.live) {
+    wv = load_param<VEC>(w, q.c0, 1.f);
+    bv = load_param<VEC>(bias, q.c0, 0.f);
+  }
+  grid_dep_wait();
+  int lanes = 32;  // of a group: all of the slab's at once
+  while (lanes * q.groups > kTileThreads) lanes /= 2;
+  const int g = threadIdx.x / lanes;
+  const int64_t id = q.n * p.G + q.g0 + (g < q.groups ? g : 0);
+  const float2 m = merged ? merged[id] : add_parts(p, k, parts, id, lanes);
+  if (threadIdx.x % lanes == 0 && g < q.groups) of_group[g] = m;
+  __syncthreads();
+  if (q.live && q.row0 + q.deep < q.row1) {
+    const int of = k.subs == 1 ? uint32_t(q.col) / uint32_t(k.per_group) : 0;
+    const float mu = mean ? mean[q.n * p.G + q.g0 + of] : 0.f, r = rstd[q.n * p.G + q.g0 + of];
+    const float m1 = of_group[of].x, m2 = of_group[of].y;
+    const int count = static_cast<int>((q.row1 - q.row0 - q.deep - 1) / k.depth) + 1;
+    const int64_t row = q.n * p.S + q.row0 + q.deep, ex = k.depth * p.sx, ez = k.depth * p.sz, ey = k.depth * p.C;
+    const IO* xp = x + row * p.sx + q.c0;
+    const IO* zp = kGated ? z + row * p.sz + q.c0 : nullptr;
+    int64_t to = row * p.C + q.c0;
+    for (int i = 0; i < count; i += kGo) {
+      Pack<IO, VEC> xr[kGo], dr[kGo], zr[kGated ? kGo : 1];
+#pragma unroll
+      for (int j = 0; j < kGo; ++j) {
+        const int64_t at = i + j < count ? j : count - 1 - i;
+        xr[j].load(xp + at * ex);
+        dr[j].load(dy + to + at * ey);
+        if constexpr (kGated) zr[j].load(zp + at * ez);
+      }
+#pragma unroll
+      for (int j = 0; j < kGo; ++j) {
+        if (i + j < count) {
+          Back<IO, VEC, ACT> v;
+          v.from(xr[j], zr[kGated ? j : 0], dr[j], mu, r, wv, bv);
+          Vals<VEC> dv = ((v.dn * wv - m1) - v.xhat * m2) * r;
+          Pack<IO, VEC> out;
+          if constexpr (ACT == SSD_NORM_GATE) {
+            out.narrow(v.slope);
+            out.store(dz + to + j * ey);
+          }
+          if constexpr (ACT == SSD_NORM_GATE_FIRST) {
+            out.narrow(dv * xr[j].widen() * v.slope);
+            out.store(dz + to + j * ey);
+            dv = dv * v.gate;
+          }
+          out.narrow(dv);
+          out.store(dx + to + j * ey);
+        }
+      }
+      xp += kGo * ex;
+      to += kGo * ey;
+      if constexpr (kGated) zp += kGo * ez;
+    }
+  }
+  grid_dep_launch();
+}
+
+// dweight and dbias: the sums of the rows of `shares`.  A CTA takes 32 of the 2 C columns, 32 threads each.
+__global__ void __launch_bounds__(1024) param_kernel(const float* __restrict__ shares, int64_t rows, int64_t C,
+                                                     float* __restrict__ dw, float* __restrict__ db) {
+  __shared__ float all[32][33];
+  const int64_t c = int64_t(blockIdx.x) * 32 + threadIdx.x % 32;
+  grid_dep_wait();
+  float s = 0.f;
+  if (c < 2 * C) {
+#pragma unroll 8
+    for (int64_t i = threadIdx.x / 32; i < rows; i += 32) s += shares[i * 2 * C + c];
+  }
+  all[threadIdx.x / 32][threadIdx.x % 32] = s;
+  __syncthreads();
+  s = lanes_sum(all[threadIdx.x % 32][threadIdx.x / 32], 32);  // a warp a column
+  const int64_t mine = int64_t(blockIdx.x) * 32 + threadIdx.x / 32;
+  if (threadIdx.x % 32 == 0 && mine < 2 * C) {
+    if (mine < C && dw) dw[mine] = s;
+    if (mine >= C && db) db[mine - C] = s;
+  }
+  grid_dep_launch();
+}
+
+constexpr int kMergeInPlace = 96;  // tiles of a group that every CTA of dx_kernel adds up by itself
+
+// Workspace: the shares of dw and db, the tiles' sums, the groups' sums
+struct Space {
+  size_t shares, parts, sums, total;
+  int64_t rows;
+};
+Space space_of(const NormProblem& p, int vec) {
+  Space s{};
+  if (rows_ok(p, vec)) {
+    s.rows = row_plan(p, vec).stride;
+    s.total = align_up(size_t(s.rows) * 2 * size_t(p.C) * 4, 256);
+    return s;
+  }
+  const Cut k = cut_of(p, vec);
+  const size_t groups = size_t(p.n) * size_t(p.G);
+  s.rows = p.n * k.chunks;
+  s.parts = align_up(size_t(s.rows) * 2 * size_t(p.C) * 4, 256);
+  s.sums = s.parts + align_up(groups * size_t(k.parts()) * sizeof(float2), 256);
+  s.total = s.sums + align_up(groups * sizeof(float2), 256);
+  return s;
+}
+
+}  // namespace
+}  // namespace norm
+
+size_t norm_bwd_workspace_bytes(const NormProblem& p) {
+  size_t most = 0;
+  for (int vec = 1; vec <= (p.io_bf16 ? 8 : 4); vec *= 2) {  // whatever the tensors' alignment allows
+    if ((p.C / p.G) % vec != 0) continue;
+    const size_t b = norm::space_of(p, vec).total;
+    most = b > most ? b : most;
+  }
+  return most;
+}
+
+cudaError_t launch_group_norm_bwd(const NormProblem& p, const void* x, const void* z, const float* w,
+                                  const float* b, const void* dy, const float* mean, const float* rstd, void* dx,
+                                  void* dz, float* dw, float* db, void* ws, cudaStream_t st) {
+  using namespace norm;
+  const int vec = pack_width(p, x, z);
+  const Space s = space_of(p, vec);
+  float* shares = reinterpret_cast<float*>(static_cast<char*>(ws) + s.shares);
+  cudaError_t e = with_types(p, vec, [&](auto io, auto v, auto act) -> cudaError_t {
+    using IO = decltype(io);
+    constexpr int VEC = decltype(v)::value, ACT = decltype(act)::value;
+    const IO* xi = static_cast<const IO*>(x);
+    const IO* zi = static_cast<const IO*>(z);
+    const IO* di = static_cast<const IO*>(dy);
+    IO* dxo = static_cast<IO*>(dx);
+    IO* dzo = static_cast<IO*>(dz);
+    if (rows_ok(p, VEC)) {
+      const RowPlan k = row_plan(p, VEC);
+#define SSD_ROWS(RR, LL) launch_rows<IO, VEC, ACT, RR, LL>(p, k, xi, zi, w, b, di, mean, rstd, dxo, dzo, shares, st)
+      if (k.lanes == 8) return SSD_ROWS(1, 8);
+      if (k.lanes == 32) return k.R == 1 ? SSD_ROWS(1, 32) : SSD_ROWS(2, 32);
+      return k.R == 1 ? SSD_ROWS(1, 0) : SSD_ROWS(2, 0);
+#undef SSD_ROWS
+    }
+    const Cut k = cut_of(p, VEC);
+    const dim3 grid(static_cast<unsigned>(p.n * k.chunks * k.slabs));
+    float2* parts = reinterpret_cast<float2*>(static_cast<char*>(ws) + s.parts);
+    float2* sums = k.parts() > kMergeInPlace ? reinterpret_cast<float2*>(static_cast<char*>(ws) + s.sums) : nullptr;
+    cudaError_t e = launch_pdl(sum_kernel<IO, VEC, ACT>, grid, dim3(kTileThreads), 0, st, p, k, xi, zi, w, b, di, mean, rstd,
+                               parts, shares);
+    if (e == cudaSuccess && sums)
+      e = launch_pdl(add_kernel, dim3(static_cast<unsigned>(ceil_div(p.n * p.G, 4))), dim3(128), 0, st, p, k,
+                     static_cast<const float2*>(parts), sums);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(dx_kernel<IO, VEC, ACT>, grid, dim3(kTileThreads), 0, st, p, k, xi, zi, w, b, di, mean, rstd, dxo, dzo,
+                      static_cast<const float2*>(parts), static_cast<const float2*>(sums));
+  });
+  if (e != cudaSuccess || (!dw && !db)) return e;
+  return launch_pdl(param_kernel, dim3(static_cast<unsigned>(ceil_div(2 * p.C, 32))), dim3(1024), 0, st,
+                    static_cast<const float*>(shares), s.rows, p.C, dw, db);
+}
+
+}  // namespace ssd
