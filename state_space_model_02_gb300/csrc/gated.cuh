@@ -313,12 +313,17 @@ inline size_t maps_bytes(const GatedProblem& p, const Plan& plan) {
 // The largest piece that every row of the tensors can be copied in.
 int piece_bytes(const GatedProblem& p, const void* x, const void* gate);
 
-// Launches kern on a grid of (columns x cluster, batch, segments), clusters along x.
 template <typename... KArgs, typename... Args_>
-cudaError_t launch(void (*kern)(KArgs...), const Plan& plan, int64_t batch, int threads, size_t smem, cudaStream_t st,
-                   Args_... args) {
-  cudaError_t e = cudaSuccess;
-  if (smem > 16 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+cudaError_t launch_config(const cudaLaunchConfig_t* cfg, void (*kern)(KArgs...), Args_... args) {
+  return cudaLaunchKernelEx(cfg, kern, static_cast<KArgs>(args)...);
+}
+
+constexpr int kMostSmem = 200 * 1024;  // the largest rings and maps of any launch fit
+
+// Launches KERN on a grid of (columns x cluster, batch, segments), clusters along x.
+template <auto KERN, typename... Args_>
+cudaError_t launch(const Plan& plan, int64_t batch, int threads, size_t smem, cudaStream_t st, Args_... args) {
+  cudaError_t e = allow_smem<KERN>(kMostSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(plan.columns * plan.cluster), static_cast<unsigned>(batch),
@@ -335,7 +340,7 @@ cudaError_t launch(void (*kern)(KArgs...), const Plan& plan, int64_t batch, int 
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = plan.cluster > 1 ? 2 : 1;
-  e = cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
+  e = launch_config(&cfg, KERN, args...);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

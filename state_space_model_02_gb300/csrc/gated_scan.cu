@@ -474,17 +474,17 @@ cudaError_t launch_gated_scan(const GatedProblem& p, const void* x, const void* 
     const IO* gi = static_cast<const IO*>(gate);
     IO* yo = static_cast<IO*>(y);
     if (plan.cluster > 1)
-      return launch(scan_kernel<IO, KIND, COMP, G, kScanWarps, TW, kSlots>, plan, p.b, (kScanWarps + 1) * 32,
+      return launch<scan_kernel<IO, KIND, COMP, G, kScanWarps, TW, kSlots>>(plan, p.b, (kScanWarps + 1) * 32,
                     kScanWarps * kSlots * 2 * tile64 + size_t(plan.cluster) * 1024, st, plan.args(p), xi, gi, init, yo,
                     final_state, states);
     if (plan.segments > 1) {
       Plan m = plan;
       m.columns = columns64(p);
-      const cudaError_t e = launch(map_kernel<IO, KIND, COMP, G, kMapWarps, TW, kSlots>, m, p.b, kMapWarps * 32,
+      const cudaError_t e = launch<map_kernel<IO, KIND, COMP, G, kMapWarps, TW, kSlots>>(m, p.b, kMapWarps * 32,
                                    kMapWarps * kSlots * 2 * tile64, st, m.args(p), xi, gi, maps);
       if (e != cudaSuccess) return e;
     }
-    return launch(chain_kernel<IO, KIND, COMP, G, kChainWarps, TW, kSlots>, plan, p.b, kChainWarps * 32,
+    return launch<chain_kernel<IO, KIND, COMP, G, kChainWarps, TW, kSlots>>(plan, p.b, kChainWarps * 32,
                   kChainWarps * (kSlots * 2 + 1) * tile32, st, plan.args(p), xi, gi, init, yo, final_state, states, maps);
   });
 }

@@ -301,11 +301,11 @@ cudaError_t launch_gated_scan_bwd(const GatedProblem& p, const void* x, const vo
     const IO* gi = static_cast<const IO*>(gate);
     const IO* di = static_cast<const IO*>(dy);
     if (plan.segments > 1) {
-      const cudaError_t e = launch(map_bwd_kernel<IO, KIND, G, NS>, plan, p.b, kWarps * 32, kWarps * NS * 2 * bytes, st, a,
+      const cudaError_t e = launch<map_bwd_kernel<IO, KIND, G, NS>>(plan, p.b, kWarps * 32, kWarps * NS * 2 * bytes, st, a,
                                    gi, di, dfinal, maps);
       if (e != cudaSuccess) return e;
     }
-    return launch(scan_bwd_kernel<IO, KIND, COMP, G, NS>, plan, p.b, kWarps * 32, 
+    return launch<scan_bwd_kernel<IO, KIND, COMP, G, NS>>(plan, p.b, kWarps * 32, 
                   kWarps * (NS * 3 + 2) * bytes + size_t(plan.cluster) * 1024, st, a, xi, gi, di,
                   states, dfinal, static_cast<IO*>(dx), static_cast<IO*>(dgate), dinit, maps);
   });

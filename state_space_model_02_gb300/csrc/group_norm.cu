@@ -11,7 +11,6 @@
 //                 first kernel read last is still in the L2 cache.  (4 x 65536 x 256, bf16: 76 us; in batches of samples that
 //                 fit in the cache 102 us, the launches cost more than the second reading.)
 #include "group_norm.cuh"
-#include <atomic>
 
 namespace ssd {
 namespace norm {
@@ -159,14 +158,16 @@ cudaError_t launch_rows(const NormProblem& p, int threads, const IO* x, const IO
   size_t smem = 0;
   if constexpr (LANES != 0) {
     smem = size_t(threads) * R * (ACT == SSD_NORM_GATE || ACT == SSD_NORM_GATE_FIRST ? 2 : 1) * kRowSlots * Pack<IO, VEC>::kBytes;
-    static std::atomic<int> known{0};  // CTAs that an SM holds; 0: not asked for yet
-    int resident = known.load(std::memory_order_relaxed);
+    cudaError_t e = allow_smem<row_kernel<IO, VEC, ACT, R, LANES>>(int(smem));
+    if (e != cudaSuccess) return e;
+    static OncePerDevice known;  // CTAs that an SM holds
+    std::atomic<int>* place = known.of_device();
+    int resident = place ? place->load(std::memory_order_relaxed) : 0;
     if (resident == 0) {
-      cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-      if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kern, threads, smem);
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kern, threads, smem);
       if (e != cudaSuccess) return e;
       resident = resident < 1 ? 1 : resident;
-      known.store(resident, std::memory_order_relaxed);
+      if (place) place->store(resident, std::memory_order_relaxed);
     }
     // teams: a multiple of the groups, as many as the SMs hold at once, and no more than there are rows to take
     per_cta = threads / LANES;

@@ -11,8 +11,6 @@
 //                     are weighted sums; then dx from the second reading, the last tiles first.
 //
 // The shares of dw and db, one row each of [2][C] in the workspace, are added up in a fixed order by param_kernel.
-#include <atomic>
-
 #include "group_norm.cuh"
 
 namespace ssd {
@@ -187,12 +185,8 @@ cudaError_t launch_rows(const NormProblem& p, const RowPlan& k, const IO* x, con
                         const IO* dy, const float* mean, const float* rstd, IO* dx, IO* dz, float* shares, cudaStream_t st) {
   auto kern = row_bwd_kernel<IO, VEC, ACT, R, LANES>;
   constexpr int kPerThread = R * (ACT == SSD_NORM_GATE || ACT == SSD_NORM_GATE_FIRST ? 3 : 2) * kRowSlots * Pack<IO, VEC>::kBytes;
-  static std::atomic<bool> known{false};
-  if (!known.load(std::memory_order_relaxed)) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 512 * kPerThread);
-    if (e != cudaSuccess) return e;
-    known.store(true, std::memory_order_relaxed);
-  }
+  const cudaError_t e = allow_smem<row_bwd_kernel<IO, VEC, ACT, R, LANES>>(512 * kPerThread);
+  if (e != cudaSuccess) return e;
   const int64_t ctas = ceil_div(k.stride * p.G, LANES ? k.threads / LANES : 1);
   return launch_pdl(kern, dim3(static_cast<unsigned>(ctas)), dim3(k.threads), size_t(k.threads) * kPerThread, st, p,
                     static_cast<int>(k.stride), x, z, w, b, dy, mean, rstd, dx, dz, shares);

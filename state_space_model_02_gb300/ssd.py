@@ -100,15 +100,15 @@ def load_library(path: str = LIB_PATH):
         "ssd_selective_scan": ([ctypes.POINTER(SelShape)] + [vp] * 10, ctypes.c_int),
         "ssd_bwd_workspace_bytes": ([sp], ctypes.c_size_t),
         "ssd_bwd": ([sp] + [vp] * 17 + [ctypes.c_size_t, vp], ctypes.c_int),
-        "ssd_gated_workspace_bytes": ([ctypes.POINTER(GatedShape)], ctypes.c_size_t),
-        "ssd_gated_scan": ([ctypes.POINTER(GatedShape)] + [vp] * 7 + [ctypes.c_size_t, vp], ctypes.c_int),
-        "ssd_gated_bwd_workspace_bytes": ([ctypes.POINTER(GatedShape)], ctypes.c_size_t),
-        "ssd_gated_scan_bwd": ([ctypes.POINTER(GatedShape)] + [vp] * 9 + [ctypes.c_size_t, vp], ctypes.c_int),
-        "ssd_gated_decode": ([ctypes.POINTER(GatedShape)] + [vp] * 6, ctypes.c_int),
-        "ssd_norm_workspace_bytes": ([ctypes.POINTER(NormShape)], ctypes.c_size_t),
-        "ssd_group_norm": ([ctypes.POINTER(NormShape)] + [vp] * 8 + [ctypes.c_size_t, vp], ctypes.c_int),
-        "ssd_norm_bwd_workspace_bytes": ([ctypes.POINTER(NormShape)], ctypes.c_size_t),
-        "ssd_group_norm_bwd": ([ctypes.POINTER(NormShape)] + [vp] * 12 + [ctypes.c_size_t, vp], ctypes.c_int),
+        "ssd_gated_workspace_bytes": ([vp], ctypes.c_size_t),
+        "ssd_gated_scan": ([vp] * 8 + [ctypes.c_size_t, vp], ctypes.c_int),
+        "ssd_gated_bwd_workspace_bytes": ([vp], ctypes.c_size_t),
+        "ssd_gated_scan_bwd": ([vp] * 10 + [ctypes.c_size_t, vp], ctypes.c_int),
+        "ssd_gated_decode": ([vp] * 7, ctypes.c_int),
+        "ssd_norm_workspace_bytes": ([vp], ctypes.c_size_t),
+        "ssd_group_norm": ([vp] * 9 + [ctypes.c_size_t, vp], ctypes.c_int),
+        "ssd_norm_bwd_workspace_bytes": ([vp], ctypes.c_size_t),
+        "ssd_group_norm_bwd": ([vp] * 13 + [ctypes.c_size_t, vp], ctypes.c_int),
         "ssd_status_str": ([ctypes.c_int], ctypes.c_char_p),
         "ssd_last_error": ([], ctypes.c_char_p),
         "ssd_kernel_plan": ([sp], ctypes.c_int),
@@ -349,15 +349,27 @@ def bwd(x, dt, A, B, C, D, dy, chunk=256, init_state=None, dfinal=None, *, works
     return out
 
 
+# The calls below are made once a token in serving, where their time on the host counts: what depends on sizes and
+# strides alone (the shape structure, its checks, the workspace bytes) is kept by these, and a raw pointer is an int.
+
+_plans = {}
+
+
+def _plan(key, make):
+    """The (shape structure, pointer to it, workspace bytes) of `key`, a tuple of sizes, strides and names."""
+    rec = _plans.get(key)
+    if rec is None:
+        if len(_plans) >= 4096:
+            _plans.clear()
+        shape, query = make()
+        rec = _plans[key] = (shape, ctypes.addressof(shape), query(ctypes.addressof(shape)) if query else 0)
+    return rec
+
+
 def _rows(t, name, like, shape):
     """Checks t against `like`'s type and device and the three sizes of `shape`; returns the elements
     between two of its rows (0: dense).  A slice of wider rows is taken as it lies."""
-    if not t.is_cuda or t.device != like.device:
-        raise ValueError("%s must be a CUDA tensor on x's device" % name)
-    if t.dtype != like.dtype:
-        raise TypeError("%s must be %s" % (name, like.dtype))
-    if t.shape != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    _like(t, name, like, shape)
     if t.is_contiguous():
         return 0
     n, rows, cols = shape
@@ -368,9 +380,19 @@ def _rows(t, name, like, shape):
     return row
 
 
-def _dense(t, name, like, dtype, shape):
+def _like(t, name, like, shape):
+    if not t.is_cuda or t.device != like.device:
+        raise ValueError("%s must be a CUDA tensor on x's device" % name)
+    if t.dtype != like.dtype:
+        raise TypeError("%s must be %s" % (name, like.dtype))
+    if t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+
+
+def _ptr(t, name, like, dtype, shape):
+    """The address of a dense tensor after its checks; None stays None."""
     if t is None:
-        return
+        return None
     if not t.is_cuda or t.device != like.device:
         raise ValueError("%s must be a CUDA tensor on x's device" % name)
     if t.dtype != dtype:
@@ -379,6 +401,7 @@ def _dense(t, name, like, dtype, shape):
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
 
 
 def _io_dtype(x):
@@ -392,22 +415,37 @@ def _io_dtype(x):
     raise TypeError("x must be bfloat16 or float32")
 
 
-def _on(x, stream):
-    """(context, stream pointer): what a call allocates inside the context belongs to the stream that its
-    kernels run on, so that memory it drops is not handed out while they still use it."""
+def _stream_of(x, stream):
+    """The raw stream of the call: ``stream``, or the current one."""
+    if stream is not None:
+        return stream.cuda_stream
     torch = _torch()
-    if stream is None:
-        return contextlib.nullcontext(), ctypes.c_void_p(torch.cuda.current_stream(x.device).cuda_stream)
-    return torch.cuda.stream(stream), ctypes.c_void_p(stream.cuda_stream)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # without a Stream object around it
+    return raw(x.device.index) if raw else torch.cuda.current_stream(x.device).cuda_stream
 
 
-def _gated_shape(x, gate, kind, complement):
-    io = _io_dtype(x)
-    if kind not in GATE_KINDS:
-        raise ValueError("kind must be one of %s" % ", ".join(GATE_KINDS))
-    b, L, D = x.shape
-    return GatedShape(b, L, D, _rows(x, "x", x, x.shape), _rows(gate, "gate", x, x.shape), io, GATE_KINDS[kind],
-                      1 if complement else 0, 0)
+def _on(stream):
+    """What a call allocates inside this context belongs to the stream that its kernels run on, so that memory it
+    drops is not handed out while they still use it."""
+    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
+
+
+def _gated_plan(x, gate, kind, complement, query):
+    # x's and gate's types and devices are not part of the key: they are looked at in every call
+    if gate.shape != x.shape or gate.dtype != x.dtype or not x.is_cuda or gate.device != x.device:
+        _like(x, "x", x, x.shape)
+        _like(gate, "gate", x, x.shape)
+
+    def make():
+        io = _io_dtype(x)
+        if kind not in GATE_KINDS:
+            raise ValueError("kind must be one of %s" % ", ".join(GATE_KINDS))
+        b, L, D = x.shape
+        shape = GatedShape(b, L, D, _rows(x, "x", x, x.shape), _rows(gate, "gate", x, x.shape), io, GATE_KINDS[kind],
+                           1 if complement else 0, 0)
+        return shape, getattr(load_library(), query) if query else None
+
+    return _plan((query, x.shape, x.stride(), gate.stride(), x.dtype, kind, bool(complement)), make)
 
 
 def gated_scan(x, gate, init_state=None, *, kind="logit", complement=False, y=None, final_state=None,
@@ -420,26 +458,26 @@ def gated_scan(x, gate, init_state=None, *, kind="logit", complement=False, y=No
     where ``complement``.  init_state (b,D) in fp32.  Work is enqueued on ``stream`` (default: current).
     """
     torch = _torch()
-    shape = _gated_shape(x, gate, kind, complement)
+    _, shape, nbytes = _gated_plan(x, gate, kind, complement, "ssd_gated_workspace_bytes")
     b, L, D = x.shape
-    ctx, st = _on(x, stream)
-    _dense(init_state, "init_state", x, torch.float32, (b, D))
-    lib = load_library()
-    nbytes = lib.ssd_gated_workspace_bytes(ctypes.byref(shape))
+    f32, dev = torch.float32, x.device
+    pi = _ptr(init_state, "init_state", x, f32, (b, D))
     states = ws = None
-    with ctx:
-        if nbytes:
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    with _on(stream):
         if y is None:
-            y = torch.empty((b, L, D), dtype=x.dtype, device=x.device)
+            y = torch.empty((b, L, D), dtype=x.dtype, device=dev)
         if final_state is None and want_final:
-            final_state = torch.empty((b, D), dtype=torch.float32, device=x.device)
+            final_state = torch.empty((b, D), dtype=f32, device=dev)
         if want_states:
-            states = torch.empty((b, -(-L // GATED_BLOCK), D), dtype=torch.float32, device=x.device)
-    _dense(y, "y", x, x.dtype, x.shape)
-    _dense(final_state, "final_state", x, torch.float32, (b, D))
-    _check(lib.ssd_gated_scan(ctypes.byref(shape), _p(x), _p(gate), _p(init_state), _p(y), _p(final_state), _p(states),
-                              _p(ws), nbytes, st))
+            states = torch.empty((b, -(-L // GATED_BLOCK), D), dtype=f32, device=dev)
+        if nbytes:
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    rc = load_library().ssd_gated_scan(shape, x.data_ptr(), gate.data_ptr(), pi, _ptr(y, "y", x, x.dtype, x.shape),
+                                       _ptr(final_state, "final_state", x, f32, (b, D)),
+                                       states.data_ptr() if want_states else None, ws.data_ptr() if nbytes else None, nbytes,
+                                       _stream_of(x, stream))
+    if rc:
+        _check(rc)
     return (y, final_state, states) if want_states else (y, final_state)
 
 
@@ -447,23 +485,24 @@ def gated_scan_bwd(x, gate, dy, states, dfinal=None, *, kind="logit", complement
     """ssd_gated_scan_bwd: gradients of gated_scan given dy (and dfinal) and the ``states`` that it returned.
     Returns a dict with dx, dgate and dinit (b,D)."""
     torch = _torch()
-    shape = _gated_shape(x, gate, kind, complement)
+    _, shape, nbytes = _gated_plan(x, gate, kind, complement, "ssd_gated_bwd_workspace_bytes")
     b, L, D = x.shape
-    ctx, st = _on(x, stream)
-    _dense(dy, "dy", x, x.dtype, x.shape)
-    _dense(states, "states", x, torch.float32, (b, -(-L // GATED_BLOCK), D))
-    _dense(dfinal, "dfinal", x, torch.float32, (b, D))
-    lib = load_library()
-    nbytes = lib.ssd_gated_bwd_workspace_bytes(ctypes.byref(shape))
+    f32, dev = torch.float32, x.device
+    pd = _ptr(dy, "dy", x, x.dtype, x.shape)
+    ps = _ptr(states, "states", x, f32, (b, -(-L // GATED_BLOCK), D))
+    pf = _ptr(dfinal, "dfinal", x, f32, (b, D))
     ws = None
-    with ctx:
-        dx = torch.empty((b, L, D), dtype=x.dtype, device=x.device)
-        dgate = torch.empty_like(dx)
-        dinit = torch.empty((b, D), dtype=torch.float32, device=x.device)
+    with _on(stream):
+        dx = torch.empty((b, L, D), dtype=x.dtype, device=dev)
+        dgate = torch.empty((b, L, D), dtype=x.dtype, device=dev)
+        dinit = torch.empty((b, D), dtype=f32, device=dev)
         if nbytes:
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-    _check(lib.ssd_gated_scan_bwd(ctypes.byref(shape), _p(x), _p(gate), _p(dy), _p(states), _p(dfinal), _p(dx),
-                                  _p(dgate), _p(dinit), _p(ws), nbytes, st))
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    rc = load_library().ssd_gated_scan_bwd(shape, x.data_ptr(), gate.data_ptr(), pd, ps, pf, dx.data_ptr(),
+                                           dgate.data_ptr(), dinit.data_ptr(), ws.data_ptr() if nbytes else None, nbytes,
+                                           _stream_of(x, stream))
+    if rc:
+        _check(rc)
     return dict(dx=dx, dgate=dgate, dinit=dinit)
 
 
@@ -471,41 +510,37 @@ def gated_decode(x, gate, state, *, kind="logit", complement=False, new_state=No
     """ssd_gated_decode: gated_scan over the few tokens of x (b,L,D) on a resident ``state`` (fp32, (b,D)),
     which is updated in place, or left as it is where ``new_state`` is given.  Returns y (b,L,D)."""
     torch = _torch()
-    shape = _gated_shape(x, gate, kind, complement)
+    _, shape, _ = _gated_plan(x, gate, kind, complement, None)
     b, L, D = x.shape
-    ctx, st = _on(x, stream)
-    if new_state is None:
-        new_state = state
-    _dense(state, "state", x, torch.float32, (b, D))
-    _dense(new_state, "new_state", x, torch.float32, (b, D))
-    with ctx:
-        if y is None:
+    ps = _ptr(state, "state", x, torch.float32, (b, D))
+    pn = ps if new_state is None else _ptr(new_state, "new_state", x, torch.float32, (b, D))
+    if y is None:
+        with _on(stream):
             y = torch.empty((b, L, D), dtype=x.dtype, device=x.device)
-    _dense(y, "y", x, x.dtype, x.shape)
-    _check(load_library().ssd_gated_decode(ctypes.byref(shape), _p(x), _p(gate), _p(state), _p(new_state), _p(y),
-                                           st))
+    rc = load_library().ssd_gated_decode(shape, x.data_ptr(), gate.data_ptr(), ps, pn,
+                                         _ptr(y, "y", x, x.dtype, x.shape), _stream_of(x, stream))
+    if rc:
+        _check(rc)
     return y
 
 
-def _norm_shape(x, z, groups, eps, act, rms):
-    io = _io_dtype(x)
-    if act not in NORM_ACTS:
-        raise ValueError("act must be one of %s" % ", ".join(NORM_ACTS))
-    gated = act in ("gate", "gate_first")
-    if gated != (z is not None):
-        raise ValueError("z goes with act='gate' and act='gate_first'")
-    n, S, C = x.shape
-    return NormShape(n, S, C, groups, _rows(x, "x", x, x.shape), _rows(z, "z", x, x.shape) if gated else 0, eps, io,
-                     NORM_ACTS[act], NORM_FLAG_RMS if rms else 0)
+def _norm_plan(x, z, groups, eps, act, rms, query):
+    if not x.is_cuda or (z is not None and (z.shape != x.shape or z.dtype != x.dtype or z.device != x.device)):
+        _like(x, "x", x, x.shape)
+        _like(z, "z", x, x.shape)
 
+    def make():
+        io = _io_dtype(x)
+        if act not in NORM_ACTS:
+            raise ValueError("act must be one of %s" % ", ".join(NORM_ACTS))
+        if (act in ("gate", "gate_first")) != (z is not None):
+            raise ValueError("z goes with act='gate' and act='gate_first'")
+        n, S, C = x.shape
+        shape = NormShape(n, S, C, groups, _rows(x, "x", x, x.shape), 0 if z is None else _rows(z, "z", x, x.shape), eps, io,
+                          NORM_ACTS[act], NORM_FLAG_RMS if rms else 0)
+        return shape, getattr(load_library(), query)
 
-def _norm_params(x, weight, bias, mean, rstd, groups):
-    torch = _torch()
-    n, _, C = x.shape
-    _dense(weight, "weight", x, torch.float32, (C,))
-    _dense(bias, "bias", x, torch.float32, (C,))
-    _dense(mean, "mean", x, torch.float32, (n, groups))
-    _dense(rstd, "rstd", x, torch.float32, (n, groups))
+    return _plan((query, x.shape, x.stride(), None if z is None else z.stride(), x.dtype, groups, eps, act, bool(rms)), make)
 
 
 def group_norm(x, weight=None, bias=None, *, groups=1, z=None, eps=1e-5, act="none", rms=False, y=None,
@@ -519,24 +554,25 @@ def group_norm(x, weight=None, bias=None, *, groups=1, z=None, eps=1e-5, act="no
     (default: current).
     """
     torch = _torch()
-    shape = _norm_shape(x, z, groups, eps, act, rms)
+    _, shape, nbytes = _norm_plan(x, z, groups, eps, act, rms, "ssd_norm_workspace_bytes")
     n, S, C = x.shape
-    lib = load_library()
-    ctx, st = _on(x, stream)
-    _norm_params(x, weight, bias, None, None, groups)
-    nbytes = lib.ssd_norm_workspace_bytes(ctypes.byref(shape))
+    f32, dev = torch.float32, x.device
+    pw, pb = _ptr(weight, "weight", x, f32, (C,)), _ptr(bias, "bias", x, f32, (C,))
     mean = rstd = ws = None
-    with ctx:
+    with _on(stream):
         if y is None:
-            y = torch.empty((n, S, C), dtype=x.dtype, device=x.device)
+            y = torch.empty((n, S, C), dtype=x.dtype, device=dev)
         if want_stats:
-            mean = torch.empty((n, groups), dtype=torch.float32, device=x.device)
-            rstd = torch.empty_like(mean)
+            mean = torch.empty((n, groups), dtype=f32, device=dev)
+            rstd = torch.empty((n, groups), dtype=f32, device=dev)
         if nbytes:
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-    _dense(y, "y", x, x.dtype, x.shape)
-    _check(lib.ssd_group_norm(ctypes.byref(shape), _p(x), _p(z), _p(weight), _p(bias), _p(y), _p(mean), _p(rstd),
-                              _p(ws), nbytes, st))
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    rc = load_library().ssd_group_norm(shape, x.data_ptr(), None if z is None else z.data_ptr(), pw, pb,
+                                       _ptr(y, "y", x, x.dtype, x.shape), mean.data_ptr() if want_stats else None,
+                                       rstd.data_ptr() if want_stats else None, ws.data_ptr() if nbytes else None, nbytes,
+                                       _stream_of(x, stream))
+    if rc:
+        _check(rc)
     return (y, mean, rstd) if want_stats else y
 
 
@@ -545,24 +581,26 @@ def group_norm_bwd(x, dy, mean, rstd, weight=None, bias=None, *, groups=1, z=Non
     """ssd_group_norm_bwd: gradients of group_norm given dy and the statistics that it returned.  Returns a dict
     with dx, dz (None without z), dweight and dbias (fp32)."""
     torch = _torch()
-    shape = _norm_shape(x, z, groups, 0.0, act, rms)
+    _, shape, nbytes = _norm_plan(x, z, groups, 0.0, act, rms, "ssd_norm_bwd_workspace_bytes")
     n, S, C = x.shape
-    lib = load_library()
-    ctx, st = _on(x, stream)
-    _dense(dy, "dy", x, x.dtype, x.shape)
-    _norm_params(x, weight, bias, mean, rstd, groups)
-    nbytes = lib.ssd_norm_bwd_workspace_bytes(ctypes.byref(shape))
+    f32, dev = torch.float32, x.device
+    pd = _ptr(dy, "dy", x, x.dtype, x.shape)
+    pw, pb = _ptr(weight, "weight", x, f32, (C,)), _ptr(bias, "bias", x, f32, (C,))
+    pm, pr = _ptr(mean, "mean", x, f32, (n, groups)), _ptr(rstd, "rstd", x, f32, (n, groups))
     dz = ws = None
-    with ctx:
-        dx = torch.empty((n, S, C), dtype=x.dtype, device=x.device)
+    with _on(stream):
+        dx = torch.empty((n, S, C), dtype=x.dtype, device=dev)
         if z is not None:
-            dz = torch.empty_like(dx)
-        dweight = torch.empty(C, dtype=torch.float32, device=x.device)
-        dbias = torch.empty_like(dweight)
+            dz = torch.empty((n, S, C), dtype=x.dtype, device=dev)
+        dweight = torch.empty((C,), dtype=f32, device=dev)
+        dbias = torch.empty((C,), dtype=f32, device=dev)
         if nbytes:
-            ws = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-    _check(lib.ssd_group_norm_bwd(ctypes.byref(shape), _p(x), _p(z), _p(weight), _p(bias), _p(dy), _p(mean),
-                                  _p(rstd), _p(dx), _p(dz), _p(dweight), _p(dbias), _p(ws), nbytes, st))
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    rc = load_library().ssd_group_norm_bwd(shape, x.data_ptr(), None if z is None else z.data_ptr(), pw, pb, pd, pm, pr,
+                                           dx.data_ptr(), None if z is None else dz.data_ptr(), dweight.data_ptr(),
+                                           dbias.data_ptr(), ws.data_ptr() if nbytes else None, nbytes, _stream_of(x, stream))
+    if rc:
+        _check(rc)
     return dict(dx=dx, dz=dz, dweight=dweight, dbias=dbias)
 
 
