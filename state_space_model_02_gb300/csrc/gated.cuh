@@ -290,15 +290,6 @@ struct Plan {
 inline int64_t columns64(const GatedProblem& p) { return (p.D + kCols - 1) / kCols; }
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// A cluster plan: as many CTAs along the sequence as fill the SMs once, `resident` on each.
-inline Plan cluster_plan(const GatedProblem& p, int64_t tile, int resident) {
-  const int64_t columns = columns64(p), tiles = ceil_div(p.L, tile);
-  int64_t K = int64_t(resident) * kSMs / (columns * p.b);
-  K = K < tiles / 2 ? K : tiles / 2;
-  K = K < 1 ? 1 : K > kMaxCluster ? kMaxCluster : K;
-  return Plan{columns, p.L, int(K), int(ceil_div(tiles, K)), 1};
-}
-
 // A plan with about `want` segments, whole multiples of `unit` tokens, walked in tiles.
 inline Plan segment_plan(const GatedProblem& p, int64_t columns, int64_t unit, int64_t want, int64_t tile) {
   const int64_t units = ceil_div(p.L, unit), run = ceil_div(units, want < 1 ? 1 : want);
@@ -319,6 +310,52 @@ cudaError_t launch_config(const cudaLaunchConfig_t* cfg, void (*kern)(KArgs...),
 }
 
 constexpr int kMostSmem = 200 * 1024;  // the largest rings and maps of any launch fit
+
+// A cluster plan for KERN.  A step of a cluster is a wait along the sequence more than it is work, so the time goes with the
+// steps that follow each other: those of a cluster, times the rounds in which the GPU, which holds so many clusters
+// of a size at once (fewer than its SMs would: a cluster stays inside one part of the chip), gets through the columns.
+// (b2 L8192 D5120, backward, 160 columns: 264 us with one CTA, 288 with two, 233, 239, 223, 246 with three to six.)
+// smem: of a CTA, by its cluster's size.
+template <auto KERN, typename F>
+cudaError_t cluster_plan(const GatedProblem& p, int64_t tile, int threads, F smem, Plan* plan) {
+  static OncePerDevice held[kMaxCluster + 1];
+  cudaError_t e = allow_smem<KERN>(kMostSmem);
+  if (e != cudaSuccess) return e;
+  const int64_t columns = columns64(p) * p.b, tiles = ceil_div(p.L, tile);
+  int64_t best = 0;
+  for (int K = 1; K <= kMaxCluster && (K == 1 || 2 * K <= tiles); ++K) {
+    std::atomic<int>* place = held[K].of_device();
+    int clusters = place ? place->load(std::memory_order_relaxed) : 0;
+    if (clusters == 0) {
+      if (K == 1) {
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&clusters, KERN, threads, smem(1));
+        clusters *= kSMs;
+      } else {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(K * kSMs);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem(K);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = K;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&clusters, KERN, &cfg);
+      }
+      if (e != cudaSuccess) return e;
+      if (clusters < 1) clusters = 1;
+      if (place) place->store(clusters, std::memory_order_relaxed);
+    }
+    const int64_t time = ceil_div(columns, clusters) * ceil_div(tiles, K);
+    if (best == 0 || time < best) {
+      best = time;
+      *plan = Plan{columns64(p), p.L, K, int(ceil_div(tiles, K)), 1};
+    }
+  }
+  return cudaSuccess;
+}
 
 // Launches KERN on a grid of (columns x cluster, batch, segments), clusters along x.
 template <auto KERN, typename... Args_>

@@ -411,20 +411,15 @@ cudaError_t launch_run(const GatedProblem& p, const void* x, const void* gate, c
 // Tokens that one thread walks rather than a cluster: a warp's tile, behind which the other warps would idle.
 constexpr int64_t kShort = 16;
 
-// Which kernel walks the sequence.  Columns of 64 channels, over the whole batch, against the 152 SMs:
-//   more than SMs       a chain for each column of 32
-//   fewer               clusters, eight CTAs at most: below kFewColumns columns they leave SMs without work, and
-//   below kFewColumns   segments, if the sequence is long enough to be worth a second reading
-// (65536 tokens, 8 columns, float32: 104 us in segments; 32768 tokens, 32 columns, bf16: 82 us in clusters.)
-constexpr int kFewColumns = 24;
-
-Plan scan_plan(const GatedProblem& p) {
-  const int64_t tile = p.io_bf16 ? kTokens<uint16_t> : kTokens<float>, columns = columns64(p) * p.b;
-  const int64_t columns32 = ceil_div(p.D, 32), unit = kMapWarps * tile;
-  if (columns < kFewColumns && p.L >= 32 * unit)
-    return segment_plan(p, columns32, unit, int64_t(kChainResident) * kSMs / (columns32 * p.b), tile);
-  const Plan q = cluster_plan(p, kScanWarps * tile, kResident);
-  return columns > kSMs || q.cluster == 1 ? Plan{columns32, p.L, 1, 1, 1} : q;
+// Columns of 64 channels, over the whole batch, below which even clusters of eight CTAs leave SMs without work: then segments,
+// if the sequence is long enough to be worth a second reading (65536 tokens, 8 columns, float32: 104 us).  With more
+// columns than SMs each column of 32 has a chain of its own.
+bool in_segments(const GatedProblem& p) {
+  return columns64(p) * p.b < 24 && p.L >= 32 * kMapWarps * (p.io_bf16 ? kTokens<uint16_t> : kTokens<float>);
+}
+Plan scan_segments(const GatedProblem& p) {
+  const int64_t tile = p.io_bf16 ? kTokens<uint16_t> : kTokens<float>, columns32 = ceil_div(p.D, 32);
+  return segment_plan(p, columns32, kMapWarps * tile, int64_t(kChainResident) * kSMs / (columns32 * p.b), tile);
 }
 
 bool aligned(const void* p, size_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
@@ -456,36 +451,43 @@ int piece_bytes(const GatedProblem& p, const void* x, const void* gate) {
 }  // namespace gated
 
 size_t gated_workspace_bytes(const GatedProblem& p) {
-  return p.L <= gated::kShort ? 0 : gated::maps_bytes(p, gated::scan_plan(p));
+  return gated::in_segments(p) ? gated::maps_bytes(p, gated::scan_segments(p)) : 0;
 }
 
 cudaError_t launch_gated_scan(const GatedProblem& p, const void* x, const void* gate, const float* init, void* y,
                               float* final_state, float* states, void* ws, cudaStream_t st) {
   using namespace gated;
   if (p.L <= kShort) return run(p, x, gate, init, y, final_state, states, st);
-  const Plan plan = scan_plan(p);
   const Maps maps{static_cast<float*>(ws), columns64(p) * kCols};
   return with_types(p, piece_bytes(p, x, gate), [&](auto io, auto g, auto kind, auto comp) {
     using IO = decltype(io);
     constexpr int G = decltype(g)::value, KIND = decltype(kind)::value, TW = kTokens<IO>;
     constexpr bool COMP = decltype(comp)::value;
+    constexpr auto clustered = scan_kernel<IO, KIND, COMP, G, kScanWarps, TW, kSlots>;
     constexpr size_t tile64 = Tile<IO, G, TW, kCols>::kBytes, tile32 = Tile<IO, G, TW, 32>::kBytes;
+    auto smem = [](int K) { return kScanWarps * kSlots * 2 * tile64 + size_t(K) * 1024; };
     const IO* xi = static_cast<const IO*>(x);
     const IO* gi = static_cast<const IO*>(gate);
     IO* yo = static_cast<IO*>(y);
-    if (plan.cluster > 1)
-      return launch<scan_kernel<IO, KIND, COMP, G, kScanWarps, TW, kSlots>>(plan, p.b, (kScanWarps + 1) * 32,
-                    kScanWarps * kSlots * 2 * tile64 + size_t(plan.cluster) * 1024, st, plan.args(p), xi, gi, init, yo,
-                    final_state, states);
-    if (plan.segments > 1) {
+    Plan plan{ceil_div(p.D, 32), p.L, 1, 1, 1};
+    cudaError_t e = cudaSuccess;
+    if (in_segments(p)) {
+      plan = scan_segments(p);
       Plan m = plan;
       m.columns = columns64(p);
-      const cudaError_t e = launch<map_kernel<IO, KIND, COMP, G, kMapWarps, TW, kSlots>>(m, p.b, kMapWarps * 32,
-                                   kMapWarps * kSlots * 2 * tile64, st, m.args(p), xi, gi, maps);
-      if (e != cudaSuccess) return e;
+      e = launch<map_kernel<IO, KIND, COMP, G, kMapWarps, TW, kSlots>>(m, p.b, kMapWarps * 32, kMapWarps * kSlots * 2 * tile64,
+                                                                       st, m.args(p), xi, gi, maps);
+    } else if (columns64(p) * p.b <= kSMs) {
+      Plan q;
+      e = cluster_plan<clustered>(p, kScanWarps * TW, (kScanWarps + 1) * 32, smem, &q);
+      if (e == cudaSuccess && q.cluster > 1)
+        return launch<clustered>(q, p.b, (kScanWarps + 1) * 32, smem(q.cluster), st, q.args(p), xi, gi, init, yo, final_state,
+                                 states);
     }
-    return launch<chain_kernel<IO, KIND, COMP, G, kChainWarps, TW, kSlots>>(plan, p.b, kChainWarps * 32,
-                  kChainWarps * (kSlots * 2 + 1) * tile32, st, plan.args(p), xi, gi, init, yo, final_state, states, maps);
+    if (e != cudaSuccess) return e;
+    return launch<chain_kernel<IO, KIND, COMP, G, kChainWarps, TW, kSlots>>(
+        plan, p.b, kChainWarps * 32, kChainWarps * (kSlots * 2 + 1) * tile32, st, plan.args(p), xi, gi, init, yo, final_state,
+        states, maps);
   });
 }
 

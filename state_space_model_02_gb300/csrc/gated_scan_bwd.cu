@@ -17,6 +17,10 @@ namespace {
 
 constexpr int kWarps = 8, kResident = 2;
 constexpr int kTok = SSD_GATED_BLOCK / kWarps;  // tokens of a warp's tile
+// Whether dx and dgate have a place of their own, so that the slot is refilled as soon as it has been read.  With float32
+// that would leave one CTA an SM: they take the slot's.
+template <typename IO>
+constexpr bool kStaged = sizeof(IO) == 2;
 
 // Adds dfinal to what the tile's last token has from dy, where that is the sequence's last.
 __device__ __forceinline__ void add_final(float2 (&d)[kTok], const float* dfinal, int64_t t0, const Args& p, int64_t b,
@@ -58,10 +62,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(
   const IO* xb = x + b * p.L * p.sx + col;
   const IO* gb = gate + b * p.L * p.sg + col;
   const IO* db = dy + b * p.L * p.D + col;
-  // shared memory: each warp's slots and the tiles its dx and dgate leave from, then the CTAs' maps of even and odd steps
-  constexpr int kWarpBytes = NS * kSlot + 2 * T::kBytes;
+  // shared memory: each warp's slots (and the tiles its dx and dgate leave from), then the CTAs' maps of even and odd steps
+  constexpr int kWarpBytes = NS * kSlot + (kStaged<IO> ? 2 * T::kBytes : 0);
   char* slots = ring + w * kWarpBytes;
-  char* stage = slots + NS * kSlot;
   float2(*cta_maps)[2][32] = reinterpret_cast<float2(*)[2][32]>(ring + kWarps * kWarpBytes);
 
   grid_dep_wait();
@@ -103,7 +106,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(
   int slot = 0;
   for (int step = p.steps - 1; step >= 0; --step) {
     const int par = step & 1;
-    const char* sl = slots + slot * kSlot;
+    char* sl = slots + slot * kSlot;
+    char* stage = kStaged<IO> ? slots + NS * kSlot : sl;
     float2(*cta_map)[2][32] = cta_maps + par * K;
     const pair_t<IO>* xs = reinterpret_cast<const pair_t<IO>*>(sl) + lane;
     const pair_t<IO>* gs = reinterpret_cast<const pair_t<IO>*>(sl + T::kBytes) + lane;
@@ -128,7 +132,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(
       R = chain_fma(P, d[i], R);
     }
     __syncwarp();
-    fetch(slot, t0 - NS * span);
+    if constexpr (kStaged<IO>) fetch(slot, t0 - NS * span);
     warp_map[par][w][0][lane] = P;
     warp_map[par][w][1][lane] = H;
     warp_map[par][w][2][lane] = R;
@@ -193,6 +197,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(
     __syncwarp();
     T::out(stage, dx + b * p.L * p.D + col, p.D, t0, end, left, lane);
     T::out(stage + T::kBytes, dgate + b * p.L * p.D + col, p.D, t0, end, left, lane);
+    if constexpr (!kStaged<IO>) {
+      __syncwarp();
+      fetch(slot, t0 - NS * span);
+    }
     t0 -= span;
     slot = slot + 1 == NS ? 0 : slot + 1;
   }
@@ -270,44 +278,47 @@ __global__ void __launch_bounds__(kWarps * 32) map_bwd_kernel(const Args p, cons
   }
 }
 
-Plan bwd_plan(const GatedProblem& p) {
-  const int64_t columns = columns64(p) * p.b;
-  if (columns < 24 && p.L >= 32 * SSD_GATED_BLOCK)
-    return segment_plan(p, columns64(p), SSD_GATED_BLOCK, int64_t(kResident) * kSMs / columns, SSD_GATED_BLOCK);
-  return cluster_plan(p, SSD_GATED_BLOCK, kResident);
+// Few columns leave SMs without work even in clusters: then segments, if the sequence is long enough to be worth a second
+// reading.
+bool in_segments(const GatedProblem& p) { return columns64(p) * p.b < 24 && p.L >= 32 * SSD_GATED_BLOCK; }
+Plan bwd_segments(const GatedProblem& p) {
+  return segment_plan(p, columns64(p), SSD_GATED_BLOCK, int64_t(kResident) * kSMs / (columns64(p) * p.b), SSD_GATED_BLOCK);
 }
 
 }  // namespace
 }  // namespace gated
 
 size_t gated_bwd_workspace_bytes(const GatedProblem& p) {
-  return gated::maps_bytes(p, gated::bwd_plan(p));
+  return gated::in_segments(p) ? gated::maps_bytes(p, gated::bwd_segments(p)) : 0;
 }
 
 cudaError_t launch_gated_scan_bwd(const GatedProblem& p, const void* x, const void* gate, const void* dy,
                                   const float* states, const float* dfinal, void* dx, void* dgate, float* dinit,
                                   void* ws, cudaStream_t st) {
   using namespace gated;
-  const Plan plan = bwd_plan(p);
-  const Args a = plan.args(p);
   const Maps maps{static_cast<float*>(ws), columns64(p) * kCols};
   return with_types(p, piece_bytes(p, x, gate), [&](auto io, auto g, auto kind, auto comp) {
     using IO = decltype(io);
-    constexpr int G = decltype(g)::value, KIND = decltype(kind)::value;
+    constexpr int G = decltype(g)::value, KIND = decltype(kind)::value, NS = 2;
     constexpr bool COMP = decltype(comp)::value;
-    constexpr int NS = 2;
+    constexpr auto kern = scan_bwd_kernel<IO, KIND, COMP, G, NS>;
     constexpr size_t bytes = Tile<IO, G, kTok, kCols>::kBytes;
+    auto smem = [](int K) { return kWarps * (NS * 3 + (kStaged<IO> ? 2 : 0)) * bytes + size_t(K) * 1024; };
     const IO* xi = static_cast<const IO*>(x);
     const IO* gi = static_cast<const IO*>(gate);
     const IO* di = static_cast<const IO*>(dy);
-    if (plan.segments > 1) {
-      const cudaError_t e = launch<map_bwd_kernel<IO, KIND, G, NS>>(plan, p.b, kWarps * 32, kWarps * NS * 2 * bytes, st, a,
-                                   gi, di, dfinal, maps);
-      if (e != cudaSuccess) return e;
+    Plan plan;
+    cudaError_t e = cudaSuccess;
+    if (in_segments(p)) {
+      plan = bwd_segments(p);
+      e = launch<map_bwd_kernel<IO, KIND, G, NS>>(plan, p.b, kWarps * 32, kWarps * NS * 2 * bytes, st, plan.args(p), gi, di,
+                                                  dfinal, maps);
+    } else {
+      e = cluster_plan<kern>(p, SSD_GATED_BLOCK, kWarps * 32, smem, &plan);
     }
-    return launch<scan_bwd_kernel<IO, KIND, COMP, G, NS>>(plan, p.b, kWarps * 32, 
-                  kWarps * (NS * 3 + 2) * bytes + size_t(plan.cluster) * 1024, st, a, xi, gi, di,
-                  states, dfinal, static_cast<IO*>(dx), static_cast<IO*>(dgate), dinit, maps);
+    if (e != cudaSuccess) return e;
+    return launch<kern>(plan, p.b, kWarps * 32, smem(plan.cluster), st, plan.args(p), xi, gi, di, states, dfinal,
+                        static_cast<IO*>(dx), static_cast<IO*>(dgate), dinit, maps);
   });
 }
 
