@@ -82,42 +82,66 @@ __device__ __forceinline__ float exp_of(float g) {
   }
 }
 
-// The decay a and s = 1 - a.  s is taken from the gate, not from a: near a = 1 the difference has lost its low
-// bits.  kS: whether s is used.
-template <typename IO, int KIND, bool kS, bool kTiny>
+// The decay a and s = 1 - a, to a rounding of float32 near a = 1 each: a state of long memory adds up a thousand times what
+// its decay is off by, and there the MUFU unit's results, good to two units or so, would cost digits (the last state of
+// 256K tokens was off by over 1e-6 with them, by 3e-7 without).  s is taken from the gate, not from a: near a = 1
+// the difference has lost its low bits.
+// 1 - exp(g) = -g q(g): for small |g| q is a series (the first term left out is g^6 / 5040 of it, under 5e-8).
+constexpr float kSmallGate = 0.25f;
+__device__ __forceinline__ float series(float g) {
+  return fmaf(g, fmaf(g, fmaf(g, fmaf(g, fmaf(g, 1.f / 720.f, 1.f / 120.f), 1.f / 24.f), 1.f / 6.f), 0.5f), 1.f);
+}
+__device__ __forceinline__ float2 series(float2 g) {
+  auto c = [](float f) { return make_float2(f, f); };
+  float2 q = fma_f32x2(g, c(1.f / 720.f), c(1.f / 120.f));
+  q = fma_f32x2(g, q, c(1.f / 24.f));
+  q = fma_f32x2(g, q, c(1.f / 6.f));
+  q = fma_f32x2(g, q, c(0.5f));
+  return fma_f32x2(g, q, c(1.f));
+}
+template <typename IO, int KIND, bool kTiny>
 __device__ __forceinline__ void gate_of(float g, float& a, float& s) {
   if constexpr (KIND == SSD_GATE_DECAY) {
     a = g;
     s = 1.f - g;
   } else if constexpr (KIND == SSD_GATE_LOG) {
-    a = exp_of<IO, kTiny>(g);
-    if constexpr (kS) {
-      // 1 - exp(g): for small |g| its series (the first term left out is g^6 / 5040 of it, under 5e-8)
-      const float q = fmaf(g, fmaf(g, fmaf(g, fmaf(g, fmaf(g, 1.f / 720.f, 1.f / 120.f), 1.f / 24.f), 1.f / 6.f), 0.5f), 1.f);
-      s = fabsf(g) < 0.25f ? -g * q : 1.f - a;
-    }
+    const float e = exp_of<IO, kTiny>(g), q = series(g);
+    const bool small = fabsf(g) < kSmallGate;
+    a = small ? fmaf(g, q, 1.f) : e;
+    s = small ? -g * q : 1.f - e;
   } else {
-    const float e = exp_of<IO, kTiny>(-g);
-    a = rcp(1.f + e);
-    if constexpr (kS) s = e > 1.f ? 1.f - a : e * a;
+    const float e = exp_of<IO, kTiny>(-g), r = rcp(1.f + e), er = e * r;
+    a = e > 1.f ? r : 1.f - er;
+    s = e > 1.f ? 1.f - r : er;
   }
 }
-template <typename IO, int KIND, bool kS, bool kTiny>
+// Of two values, where the pipes can two at a time.
+template <typename IO, int KIND, bool kTiny>
 __device__ __forceinline__ void gate_of(float2 g, float2& a, float2& s) {
-  if constexpr (KIND == SSD_GATE_LOGIT && sizeof(IO) == 2) {  // the same, two at a time where the pipes can
-    constexpr float kScale = (kTiny ? -0.5f : -1.f) * kLog2eHi;
-    const float2 z = mul_f32x2(g, make_float2(kScale, kScale));
-    float2 e = make_float2(ex2(z.x), ex2(z.y));
-    if constexpr (kTiny) e = mul_f32x2(e, e);
-    const float2 d = vadd(e, make_float2(1.f, 1.f));
-    a = make_float2(rcp(d.x), rcp(d.y));
-    if constexpr (kS) {
-      const float2 ea = mul_f32x2(e, a), na = vsub(make_float2(1.f, 1.f), a);
-      s = make_float2(e.x > 1.f ? na.x : ea.x, e.y > 1.f ? na.y : ea.y);
-    }
+  const float2 one = make_float2(1.f, 1.f);
+  if constexpr (KIND == SSD_GATE_DECAY) {
+    a = g;
+    s = vsub(one, g);
+  } else if constexpr (KIND == SSD_GATE_LOG) {
+    const float2 e = make_float2(exp_of<IO, kTiny>(g.x), exp_of<IO, kTiny>(g.y)), q = series(g);
+    const float2 near = fma_f32x2(g, q, one), gq = mul_f32x2(g, q), se = vsub(one, e);
+    const bool sx = fabsf(g.x) < kSmallGate, sy = fabsf(g.y) < kSmallGate;
+    a = make_float2(sx ? near.x : e.x, sy ? near.y : e.y);
+    s = make_float2(sx ? -gq.x : se.x, sy ? -gq.y : se.y);
   } else {
-    gate_of<IO, KIND, kS, kTiny>(g.x, a.x, s.x);
-    gate_of<IO, KIND, kS, kTiny>(g.y, a.y, s.y);
+    float2 e;
+    if constexpr (sizeof(IO) == 2) {
+      constexpr float kScale = (kTiny ? -0.5f : -1.f) * kLog2eHi;
+      const float2 z = mul_f32x2(g, make_float2(kScale, kScale));
+      e = make_float2(ex2(z.x), ex2(z.y));
+      if constexpr (kTiny) e = mul_f32x2(e, e);
+    } else {
+      e = make_float2(exp_of<IO, kTiny>(-g.x), exp_of<IO, kTiny>(-g.y));
+    }
+    const float2 d = vadd(e, one), r = make_float2(rcp(d.x), rcp(d.y)), er = mul_f32x2(e, r);
+    const float2 nr = vsub(one, r), ner = vsub(one, er);
+    a = make_float2(e.x > 1.f ? r.x : ner.x, e.y > 1.f ? r.y : ner.y);
+    s = make_float2(e.x > 1.f ? nr.x : er.x, e.y > 1.f ? nr.y : er.y);
   }
 }
 

@@ -138,7 +138,7 @@ __global__ void __launch_bounds__((NW + 1) * 32, kResident) scan_kernel(
     float2 a[TW], u[TW], s, P = make_float2(1.f, 1.f), H = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < TW; ++i) {
-      gate_of<IO, KIND, COMP, false>(widen(gs[i * 32]), a[i], s);
+      gate_of<IO, KIND, false>(widen(gs[i * 32]), a[i], s);
       u[i] = widen(xs[i * 32]);
       if constexpr (COMP) u[i] = mul_f32x2(u[i], s);
       H = chain_fma(a[i], H, u[i]);
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(NW * 32, kChainResident) chain_kernel(
     float2 a[TW / 2], u[TW / 2], s;  // of two tokens
 #pragma unroll
     for (int i = 0; i < TW / 2; ++i) {
-      gate_of<IO, KIND, COMP, false>(make_float2(widen(gs[i * 64]), widen(gs[i * 64 + 32])), a[i], s);
+      gate_of<IO, KIND, false>(make_float2(widen(gs[i * 64]), widen(gs[i * 64 + 32])), a[i], s);
       u[i] = make_float2(widen(xs[i * 64]), widen(xs[i * 64 + 32]));
       if constexpr (COMP) u[i] = mul_f32x2(u[i], s);
     }
@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(NW * 32) map_kernel(const Args p, const IO* __
 #pragma unroll
       for (int i = 0; i < TW; ++i) {
         float2 a, s, u = widen(xs[i * 32]);
-        gate_of<IO, KIND, COMP, false>(widen(gs[i * 32]), a, s);
+        gate_of<IO, KIND, false>(widen(gs[i * 32]), a, s);
         if constexpr (COMP) u = mul_f32x2(u, s);
         H = chain_fma(a, H, u);
         P = chain_mul(P, a);
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(128) run_kernel(const Args p, const IO* __rest
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if (states && t % SSD_GATED_BLOCK == 0) states[(b * blocks + t / SSD_GATED_BLOCK) * p.D + c + v] = h[v];
-      gate_of<IO, KIND, COMP, false>(g[v], a, s);
+      gate_of<IO, KIND, false>(g[v], a, s);
       h[v] = fmaf(a, h[v], COMP ? s * xv[v] : xv[v]);
     }
     if constexpr (V == 2)

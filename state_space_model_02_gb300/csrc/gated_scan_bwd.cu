@@ -39,7 +39,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(
     const float* __restrict__ states, const float* __restrict__ dfinal, IO* __restrict__ dx, IO* __restrict__ dgate,
     float* __restrict__ dinit, const Maps maps) {
   using T = Tile<IO, G, kTok, kCols>;
-  constexpr bool kS = COMP || KIND == SSD_GATE_LOGIT;
   constexpr int kSlot = 3 * T::kBytes;
   extern __shared__ __align__(128) char ring[];
   __shared__ float2 warp_map[2][kWarps][3][32];
@@ -120,7 +119,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(
     float2 P = make_float2(1.f, 1.f), H = make_float2(0.f, 0.f), R = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < kTok; ++i) {
-      gate_of<IO, KIND, kS, true>(widen(gs[i * 32]), a[i], s[i]);
+      gate_of<IO, KIND, true>(widen(gs[i * 32]), a[i], s[i]);
       xv[i] = widen(xs[i * 32]);
       d[i] = widen(ds[i * 32]);
       H = chain_fma(a[i], H, COMP ? mul_f32x2(xv[i], s[i]) : xv[i]);
@@ -249,7 +248,7 @@ __global__ void __launch_bounds__(kWarps * 32) map_bwd_kernel(const Args p, cons
       float2 d[kTok], a[kTok], s;
 #pragma unroll
       for (int i = 0; i < kTok; ++i) {
-        gate_of<IO, KIND, false, true>(widen(gs[i * 32]), a[i], s);
+        gate_of<IO, KIND, true>(widen(gs[i * 32]), a[i], s);
         d[i] = widen(ds[i * 32]);
       }
       add_final(d, dfinal, t, p, b, c);
