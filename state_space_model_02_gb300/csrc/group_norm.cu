@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(kTileThreads) stat_kernel(const NormProblem p,
   constexpr bool kFirst = ACT == SSD_NORM_GATE_FIRST;
   constexpr int kGo = kFirst ? kAhead / 2 : kAhead;
   __shared__ Stat all[kTileThreads];
-  const Place q = place_of<false>(p, k, VEC);
+  const Place q = place_of(p, k, VEC, blockIdx.x);
   grid_dep_wait();
   Vals<VEC> at = splat<VEC>(0.f), s = at, ss = at;
   int count = 0;
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kTileThreads) apply_kernel(const NormProblem p
                                                              const float2* __restrict__ stats) {
   constexpr bool kGated = ACT == SSD_NORM_GATE || ACT == SSD_NORM_GATE_FIRST;
   __shared__ float2 of_group[kTileThreads];
-  const Place q = place_of<true>(p, k, VEC);
+  const Place q = place_of(p, k, VEC, gridDim.x - 1 - blockIdx.x);
   Vals<VEC> wv, bv;
   if (q.live) {
     wv = load_param<VEC>(w, q.c0, 1.f);

@@ -321,19 +321,18 @@ inline Cut cut_of(const NormProblem& p, int vec) {
   return k;
 }
 
-// The tile of a CTA and the thread's place in it.  blockIdx.x counts slabs, then chunks, then samples.
+// The tile of a CTA and the thread's place in it.  Tiles are counted by slabs, then chunks, then samples.
 struct Place {
   int64_t n, row0, row1, c0;  // c0: the thread's first channel
   int slab, chunk;
   int col, deep, g0, groups, sub;          // column of packs and position of the thread; groups of the slab
   bool live;
 };
-// kBack: the tiles in the other order, so that what the kernel before read last, and the L2 cache still has, comes
+// A second kernel takes the tiles in the other order: what the first one read last, and the L2 cache still has, comes
 // first.
-template <bool kBack>
-__device__ __forceinline__ Place place_of(const NormProblem& p, const Cut& k, int vec) {
+__device__ __forceinline__ Place place_of(const NormProblem& p, const Cut& k, int vec, uint32_t at) {
   Place q;
-  const uint32_t at = kBack ? gridDim.x - 1 - blockIdx.x : blockIdx.x, slabs = k.slabs, chunks = k.chunks;  // 32-bit divisions
+  const uint32_t slabs = k.slabs, chunks = k.chunks;  // 32-bit divisions
   q.slab = at % slabs;
   q.chunk = at / slabs % chunks;
   q.n = at / slabs / chunks;

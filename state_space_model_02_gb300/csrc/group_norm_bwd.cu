@@ -10,7 +10,7 @@
 //   sum_kernel, dx_kernel   a group spans positions: per tile and channel the sums of dn and dn xhat, of which a group's means
 //                     are weighted sums; then dx from the second reading, the last tiles first.
 //
-// The shares of dw and db, one row each of [2][C] in the workspace, are added up in a fixed order by param_kernel.
+// The shares of dw and db, one row each of [2][C] in the workspace, are added up in a fixed order behind that.
 #include "group_norm.cuh"
 
 namespace ssd {
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kTileThreads) sum_kernel(const NormProblem p, 
   constexpr int kGo = kAhead / 2;
   __shared__ Vals<VEC> all[2][kTileThreads];
   __shared__ float2 sums[kTileThreads];
-  const Place q = place_of<false>(p, k, VEC);
+  const Place q = place_of(p, k, VEC, blockIdx.x);
   Vals<VEC> wv = splat<VEC>(0.f), bv = wv, sw = wv, sb = wv;
   if (q.live) {
     wv = load_param<VEC>(w, q.c0, 1.f);
@@ -304,6 +304,37 @@ __global__ void __launch_bounds__(128) add_kernel(const NormProblem p, const Cut
   }
 }
 
+// dweight and dbias: the sums of the rows of `shares`, each [2][C].  A CTA takes 32 of the 2 C columns, THREADS / 32 threads
+// each, in a fixed order.
+template <int THREADS>
+__device__ __forceinline__ void sum_shares(int64_t cta, const float* shares, int64_t rows, int64_t C, float* dw, float* db,
+                                           float (*all)[33]) {
+  constexpr int kDeep = THREADS / 32;
+  const int64_t c = cta * 32 + threadIdx.x % 32;
+  float s = 0.f;
+  if (c < 2 * C) {
+#pragma unroll 8
+    for (int64_t i = threadIdx.x / 32; i < rows; i += kDeep) s += shares[i * 2 * C + c];
+  }
+  all[threadIdx.x / 32][threadIdx.x % 32] = s;
+  __syncthreads();
+  if (threadIdx.x < 32 && c < 2 * C) {
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < kDeep; ++i) s += all[i][threadIdx.x];
+    if (c < C && dw) dw[c] = s;
+    if (c >= C && db) db[c - C] = s;
+  }
+}
+__global__ void __launch_bounds__(1024) param_kernel(const float* __restrict__ shares, int64_t rows, int64_t C,
+                                                     float* __restrict__ dw, float* __restrict__ db) {
+  __shared__ float all[32][33];
+  grid_dep_wait();
+  sum_shares<1024>(blockIdx.x, shares, rows, C, dw, db, all);
+  grid_dep_launch();
+}
+
+// The first `param_ctas` CTAs add up the shares of dw and db.
 template <typename IO, int VEC, int ACT>
 __global__ void __launch_bounds__(kTileThreads) dx_kernel(const NormProblem p, const Cut k, const IO* __restrict__ x,
                                                           const IO* __restrict__ z, const float* __restrict__ w,
@@ -311,11 +342,20 @@ __global__ void __launch_bounds__(kTileThreads) dx_kernel(const NormProblem p, c
                                                           const float* __restrict__ mean,
                                                           const float* __restrict__ rstd, IO* __restrict__ dx,
                                                           IO* __restrict__ dz, const float2* __restrict__ parts,
-                                                          const float2* __restrict__ merged) {
+                                                          const float2* __restrict__ merged, int param_ctas,
+                                                          const float* __restrict__ shares, int64_t share_rows,
+                                                          float* __restrict__ dw, float* __restrict__ db) {
   constexpr bool kGated = ACT == SSD_NORM_GATE || ACT == SSD_NORM_GATE_FIRST;
   constexpr int kGo = kAhead / 2;
   __shared__ float2 of_group[kTileThreads];
-  const Place q = place_of<true>(p, k, VEC);
+  __shared__ float all[kTileThreads / 32][33];
+  if (static_cast<int>(blockIdx.x) < param_ctas) {
+    grid_dep_wait();
+    sum_shares<kTileThreads>(blockIdx.x, shares, share_rows, p.C, dw, db, all);
+    grid_dep_launch();
+    return;
+  }
+  const Place q = place_of(p, k, VEC, gridDim.x - 1 - blockIdx.x);
   Vals<VEC> wv, bv;
   if (q.live) {
     wv = load_param<VEC>(w, q.c0, 1.f);
@@ -371,28 +411,6 @@ __global__ void __launch_bounds__(kTileThreads) dx_kernel(const NormProblem p, c
       to += kGo * ey;
       if constexpr (kGated) zp += kGo * ez;
     }
-  }
-  grid_dep_launch();
-}
-
-// dweight and dbias: the sums of the rows of `shares`.  A CTA takes 32 of the 2 C columns, 32 threads each.
-__global__ void __launch_bounds__(1024) param_kernel(const float* __restrict__ shares, int64_t rows, int64_t C,
-                                                     float* __restrict__ dw, float* __restrict__ db) {
-  __shared__ float all[32][33];
-  const int64_t c = int64_t(blockIdx.x) * 32 + threadIdx.x % 32;
-  grid_dep_wait();
-  float s = 0.f;
-  if (c < 2 * C) {
-#pragma unroll 8
-    for (int64_t i = threadIdx.x / 32; i < rows; i += 32) s += shares[i * 2 * C + c];
-  }
-  all[threadIdx.x / 32][threadIdx.x % 32] = s;
-  __syncthreads();
-  s = lanes_sum(all[threadIdx.x % 32][threadIdx.x / 32], 32);  // a warp a column
-  const int64_t mine = int64_t(blockIdx.x) * 32 + threadIdx.x / 32;
-  if (threadIdx.x % 32 == 0 && mine < 2 * C) {
-    if (mine < C && dw) dw[mine] = s;
-    if (mine >= C && db) db[mine - C] = s;
   }
   grid_dep_launch();
 }
@@ -466,10 +484,12 @@ cudaError_t launch_group_norm_bwd(const NormProblem& p, const void* x, const voi
       e = launch_pdl(add_kernel, dim3(static_cast<unsigned>(ceil_div(p.n * p.G, 4))), dim3(128), 0, st, p, k,
                      static_cast<const float2*>(parts), sums);
     if (e != cudaSuccess) return e;
-    return launch_pdl(dx_kernel<IO, VEC, ACT>, grid, dim3(kTileThreads), 0, st, p, k, xi, zi, w, b, di, mean, rstd, dxo, dzo,
-                      static_cast<const float2*>(parts), static_cast<const float2*>(sums));
+    const unsigned param_ctas = dw || db ? static_cast<unsigned>(ceil_div(2 * p.C, 32)) : 0;
+    return launch_pdl(dx_kernel<IO, VEC, ACT>, dim3(grid.x + param_ctas), dim3(kTileThreads), 0, st, p, k, xi, zi, w, b, di,
+                      mean, rstd, dxo, dzo, static_cast<const float2*>(parts), static_cast<const float2*>(sums),
+                      static_cast<int>(param_ctas), static_cast<const float*>(shares), s.rows, dw, db);
   });
-  if (e != cudaSuccess || (!dw && !db)) return e;
+  if (e != cudaSuccess || (!dw && !db) || !rows_ok(p, vec)) return e;
   return launch_pdl(param_kernel, dim3(static_cast<unsigned>(ceil_div(2 * p.C, 32))), dim3(1024), 0, st,
                     static_cast<const float*>(shares), s.rows, p.C, dw, db);
 }
