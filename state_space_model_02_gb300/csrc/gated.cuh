@@ -342,14 +342,14 @@ constexpr int kMostSmem = 200 * 1024;  // the largest rings and maps of any laun
 // smem: of a CTA, by its cluster's size.
 template <auto KERN, typename F>
 cudaError_t cluster_plan(const GatedProblem& p, int64_t tile, int threads, F smem, Plan* plan) {
-  static OncePerDevice held[kMaxCluster + 1];
+  static OncePerDevice<kMaxCluster + 1> held;  // clusters that the GPU holds, by their size
   cudaError_t e = allow_smem<KERN>(kMostSmem);
   if (e != cudaSuccess) return e;
   const int64_t columns = columns64(p) * p.b, tiles = ceil_div(p.L, tile);
+  std::atomic<int>* known = held.of_device();
   int64_t best = 0;
   for (int K = 1; K <= kMaxCluster && (K == 1 || 2 * K <= tiles); ++K) {
-    std::atomic<int>* place = held[K].of_device();
-    int clusters = place ? place->load(std::memory_order_relaxed) : 0;
+    int clusters = known ? known[K].load(std::memory_order_relaxed) : 0;
     if (clusters == 0) {
       if (K == 1) {
         e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&clusters, KERN, threads, smem(1));
@@ -370,7 +370,7 @@ cudaError_t cluster_plan(const GatedProblem& p, int64_t tile, int threads, F sme
       }
       if (e != cudaSuccess) return e;
       if (clusters < 1) clusters = 1;
-      if (place) place->store(clusters, std::memory_order_relaxed);
+      if (known) known[K].store(clusters, std::memory_order_relaxed);
     }
     const int64_t time = ceil_div(columns, clusters) * ceil_div(tiles, K);
     if (best == 0 || time < best) {

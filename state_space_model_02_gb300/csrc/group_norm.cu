@@ -160,7 +160,7 @@ cudaError_t launch_rows(const NormProblem& p, int threads, const IO* x, const IO
     smem = size_t(threads) * R * (ACT == SSD_NORM_GATE || ACT == SSD_NORM_GATE_FIRST ? 2 : 1) * kRowSlots * Pack<IO, VEC>::kBytes;
     cudaError_t e = allow_smem<row_kernel<IO, VEC, ACT, R, LANES>>(int(smem));
     if (e != cudaSuccess) return e;
-    static OncePerDevice known;  // CTAs that an SM holds
+    static OncePerDevice<> known;  // CTAs that an SM holds
     std::atomic<int>* place = known.of_device();
     int resident = place ? place->load(std::memory_order_relaxed) : 0;
     if (resident == 0) {

@@ -92,20 +92,21 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
 // Default limit of one bounded on-chip wait (ns).
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
 
-// A number that is found out once for each device, 0 before: `of_device` is the current one's place.
+// Numbers that are found out once for each device, 0 before.
+template <int N = 1>
 struct OncePerDevice {
   static constexpr int kDevices = 64;
-  std::atomic<int> values[kDevices];
-  std::atomic<int>* of_device() {
+  std::atomic<int> values[kDevices][N];
+  std::atomic<int>* of_device() {  // the current one's
     int dev = 0;
-    return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kDevices ? &values[dev] : nullptr;
+    return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < kDevices ? values[dev] : nullptr;
   }
 };
 
 // Lets KERN have up to `bytes` of dynamic shared memory, a constant of the kernel.
 template <auto KERN>
 cudaError_t allow_smem(int bytes) {
-  static OncePerDevice done;
+  static OncePerDevice<> done;
   std::atomic<int>* d = done.of_device();
   if (d && d->load(std::memory_order_relaxed) == bytes) return cudaSuccess;
   const cudaError_t e = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);

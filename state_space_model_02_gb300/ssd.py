@@ -4,7 +4,6 @@ Every step of the forward scan runs in the library's CUDA kernels; PyTorch only
 provides device memory and the current stream.  If the library is missing the
 first call raises -- there is no fallback.
 """
-import contextlib
 import ctypes
 import os
 import warnings
@@ -424,10 +423,23 @@ def _stream_of(x, stream):
     return raw(x.device.index) if raw else torch.cuda.current_stream(x.device).cuda_stream
 
 
+class _Here:
+    """The context of calls on the current stream."""
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *_):
+        pass
+
+
+_here = _Here()
+
+
 def _on(stream):
     """What a call allocates inside this context belongs to the stream that its kernels run on, so that memory it
     drops is not handed out while they still use it."""
-    return contextlib.nullcontext() if stream is None else _torch().cuda.stream(stream)
+    return _here if stream is None else _torch().cuda.stream(stream)
 
 
 def _gated_plan(x, gate, kind, complement, query):
@@ -462,20 +474,23 @@ def gated_scan(x, gate, init_state=None, *, kind="logit", complement=False, y=No
     b, L, D = x.shape
     f32, dev = torch.float32, x.device
     pi = _ptr(init_state, "init_state", x, f32, (b, D))
-    states = ws = None
+    py = _ptr(y, "y", x, x.dtype, x.shape)
+    pf = _ptr(final_state, "final_state", x, f32, (b, D))
+    ps = pw = None
     with _on(stream):
-        if y is None:
+        if py is None:
             y = torch.empty((b, L, D), dtype=x.dtype, device=dev)
-        if final_state is None and want_final:
+            py = y.data_ptr()
+        if pf is None and want_final:
             final_state = torch.empty((b, D), dtype=f32, device=dev)
+            pf = final_state.data_ptr()
         if want_states:
             states = torch.empty((b, -(-L // GATED_BLOCK), D), dtype=f32, device=dev)
+            ps = states.data_ptr()
         if nbytes:
             ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    rc = load_library().ssd_gated_scan(shape, x.data_ptr(), gate.data_ptr(), pi, _ptr(y, "y", x, x.dtype, x.shape),
-                                       _ptr(final_state, "final_state", x, f32, (b, D)),
-                                       states.data_ptr() if want_states else None, ws.data_ptr() if nbytes else None, nbytes,
-                                       _stream_of(x, stream))
+            pw = ws.data_ptr()
+    rc = load_library().ssd_gated_scan(shape, x.data_ptr(), gate.data_ptr(), pi, py, pf, ps, pw, nbytes, _stream_of(x, stream))
     if rc:
         _check(rc)
     return (y, final_state, states) if want_states else (y, final_state)
@@ -514,11 +529,12 @@ def gated_decode(x, gate, state, *, kind="logit", complement=False, new_state=No
     b, L, D = x.shape
     ps = _ptr(state, "state", x, torch.float32, (b, D))
     pn = ps if new_state is None else _ptr(new_state, "new_state", x, torch.float32, (b, D))
-    if y is None:
+    py = _ptr(y, "y", x, x.dtype, x.shape)
+    if py is None:
         with _on(stream):
             y = torch.empty((b, L, D), dtype=x.dtype, device=x.device)
-    rc = load_library().ssd_gated_decode(shape, x.data_ptr(), gate.data_ptr(), ps, pn,
-                                         _ptr(y, "y", x, x.dtype, x.shape), _stream_of(x, stream))
+        py = y.data_ptr()
+    rc = load_library().ssd_gated_decode(shape, x.data_ptr(), gate.data_ptr(), ps, pn, py, _stream_of(x, stream))
     if rc:
         _check(rc)
     return y
@@ -558,18 +574,20 @@ def group_norm(x, weight=None, bias=None, *, groups=1, z=None, eps=1e-5, act="no
     n, S, C = x.shape
     f32, dev = torch.float32, x.device
     pw, pb = _ptr(weight, "weight", x, f32, (C,)), _ptr(bias, "bias", x, f32, (C,))
-    mean = rstd = ws = None
+    py = _ptr(y, "y", x, x.dtype, x.shape)
+    pm = pr = ps = None
     with _on(stream):
-        if y is None:
+        if py is None:
             y = torch.empty((n, S, C), dtype=x.dtype, device=dev)
+            py = y.data_ptr()
         if want_stats:
             mean = torch.empty((n, groups), dtype=f32, device=dev)
             rstd = torch.empty((n, groups), dtype=f32, device=dev)
+            pm, pr = mean.data_ptr(), rstd.data_ptr()
         if nbytes:
             ws = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-    rc = load_library().ssd_group_norm(shape, x.data_ptr(), None if z is None else z.data_ptr(), pw, pb,
-                                       _ptr(y, "y", x, x.dtype, x.shape), mean.data_ptr() if want_stats else None,
-                                       rstd.data_ptr() if want_stats else None, ws.data_ptr() if nbytes else None, nbytes,
+            ps = ws.data_ptr()
+    rc = load_library().ssd_group_norm(shape, x.data_ptr(), None if z is None else z.data_ptr(), pw, pb, py, pm, pr, ps, nbytes,
                                        _stream_of(x, stream))
     if rc:
         _check(rc)
