@@ -83,9 +83,10 @@ __device__ __forceinline__ float exp_of(float g) {
 }
 
 // The decay a and s = 1 - a, to a rounding of float32 near a = 1 each: a state of long memory adds up a thousand times what
-// its decay is off by, and there the MUFU unit's results, good to two units or so, would cost digits (the last state of
-// 256K tokens was off by over 1e-6 with them, by 3e-7 without).  s is taken from the gate, not from a: near a = 1
-// the difference has lost its low bits.
+// its decay is off by, and there the MUFU unit's results, good to two units or so, would cost digits: the last state of
+// 256K tokens, decay exp(gate), differs from float64 by 1.9e-6 (rms, relative) with them, by 2.0e-7 without, and by 3.2e-7
+// in a plain float32 scan.  It costs the scan up to 13% (32768 x 2048: 82.5 -> 93.1 us).  s is taken from the gate, not
+// from a: near a = 1 the difference has lost its low bits.
 // 1 - exp(g) = -g q(g): for small |g| q is a series (the first term left out is g^6 / 5040 of it, under 5e-8).
 constexpr float kSmallGate = 0.25f;
 __device__ __forceinline__ float series(float g) {
@@ -267,17 +268,16 @@ __device__ __forceinline__ void st_peer(uint32_t addr, float2 v) {
 
 constexpr int kCols = 64;  // channels of a cluster's column
 
-// Composes the maps of a CTA's warps, the first token's warp first (kBack: last), and writes the product P and the end
-// value into this CTA's place in every CTA of the cluster.  warp_map: P, then the forward value, or at 2 the adjoint's.
-template <bool kBack, int NW, int kParts>
-__device__ __forceinline__ void publish_map(float2 (*cta_map)[2][32], const float2 (&warp_map)[NW][kParts][32],
-                                            int rank, int K, int lane) {
+// Composes the adjoint's maps of a CTA's warps, the last token's warp first, and writes the product P and the end value
+// into this CTA's place in every CTA of the cluster.  warp_map: P, H, R.
+template <int NW>
+__device__ __forceinline__ void publish_map(float2 (*cta_map)[2][32], const float2 (&warp_map)[NW][3][32], int rank, int K,
+                                            int lane) {
   float2 P = make_float2(1.f, 1.f), H = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int i = 0; i < NW; ++i) {
-    const int k = kBack ? NW - 1 - i : i;
+  for (int k = NW - 1; k >= 0; --k) {
     const float2 kp = warp_map[k][0][lane];
-    H = fma_f32x2(kp, H, warp_map[k][kBack ? 2 : 1][lane]);
+    H = fma_f32x2(kp, H, warp_map[k][2][lane]);
     P = mul_f32x2(P, kp);
   }
   const uint32_t at = smem_u32(&cta_map[rank][0][lane]);
@@ -338,7 +338,7 @@ constexpr int kMostSmem = 200 * 1024;  // the largest rings and maps of any laun
 // A cluster plan for KERN.  A step of a cluster is a wait along the sequence more than it is work, so the time goes with the
 // steps that follow each other: those of a cluster, times the rounds in which the GPU, which holds so many clusters
 // of a size at once (fewer than its SMs would: a cluster stays inside one part of the chip), gets through the columns.
-// (b2 L8192 D5120, backward, 160 columns: 264 us with one CTA, 288 with two, 233, 239, 223, 246 with three to six.)
+// (b2 L8192 D5120, backward, 160 columns: 274 us with one CTA, 304 with two, 245, 249, 233, 255, 272, 244 with three to eight.)
 // smem: of a CTA, by its cluster's size.
 template <auto KERN, typename F>
 cudaError_t cluster_plan(const GatedProblem& p, int64_t tile, int threads, F smem, Plan* plan) {

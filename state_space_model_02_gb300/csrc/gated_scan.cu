@@ -19,7 +19,7 @@
 //                 enough to fill the SMs.
 //   map_kernel    with few columns the sequence is cut into segments, each of them reduced to its map here; chain_kernel
 //                 then starts each segment from the maps before it.  x and gate are read twice.
-//   run_kernel    a few tokens: one thread walks its channels.
+//   run_kernel    a few tokens, or many short sequences: one thread walks its channels.
 //
 #include "gated.cuh"
 
@@ -32,7 +32,8 @@ template <typename IO>
 constexpr int kTokens = sizeof(IO) == 2 ? 16 : 8;
 constexpr int kSlots = 2;
 // Warps with tokens of a cluster's CTA and CTAs that an SM holds: 7 and the exchanging warp fill the registers twice
-// over (4 + 1 warps with four CTAs leave 96 registers a thread: 129 us against 82 for 32768 tokens of 2048 channels)
+// over (4 + 1 warps with four CTAs leave 96 registers a thread: 129 us against 82 for 32768 tokens of 2048 channels, the decays
+// straight from the MUFU unit)
 constexpr int kScanWarps = 7, kResident = 2;
 // The same of a chain's CTA
 constexpr int kChainWarps = 8, kChainResident = 3, kMapWarps = 8;
@@ -49,7 +50,9 @@ __device__ __forceinline__ void narrow_to(uint16_t* p, uint16_t* q, float2 f) {
 
 // The exchanging warp alone publishes (releases) at the cluster's barrier: a release waits for the stores to global
 // memory that its thread has under way, and this warp has none.  (With the exchange done by a warp that also writes
-// y, and every warp folding the maps before its own: 103 us against 82 for 32768 tokens of 2048 channels.)
+// y, and every warp folding the maps before its own: 103 us against 82 for 32768 tokens of 2048 channels, the decays
+// straight from the MUFU unit.)  bf16: 32768 x 2048 93 us (64% of the measured copy bandwidth), 262144 x 2048 714 us
+// (66%): 4.0 of 8.5 warp cycles an issue are the wait for the maps.
 template <typename IO, int KIND, bool COMP, int G, int NW, int TW, int NS>
 __global__ void __launch_bounds__((NW + 1) * 32, kResident) scan_kernel(
     const Args p, const IO* __restrict__ x, const IO* __restrict__ gate, const float* __restrict__ init,
@@ -181,7 +184,8 @@ __global__ void __launch_bounds__((NW + 1) * 32, kResident) scan_kernel(
 
 // The state goes from warp to warp through shared memory and a barrier of the two warps alone; what a tile needs beside
 // it is in registers by then.  Columns of 32 channels rather than 64: their CTAs are smaller, so that more of them
-// share the SMs evenly (b2 L8192 D5120, 160 columns of 64: 100 us both; b4, 320 columns: 170 against 205 us).
+// share the SMs evenly (b4 L8192 D5120, bf16: 170 against 205 us, b2 100 and 101, the decays straight from the MUFU
+// unit).  b4 L8192 D5120 188 us (79% of the measured copy bandwidth), b2 with float32 164 us (91%).
 template <typename IO, int KIND, bool COMP, int G, int NW, int TW, int NS>
 __global__ void __launch_bounds__(NW * 32, kChainResident) chain_kernel(
     const Args p, const IO* __restrict__ x, const IO* __restrict__ gate, const float* __restrict__ init,
@@ -408,12 +412,20 @@ cudaError_t launch_run(const GatedProblem& p, const void* x, const void* gate, c
                     static_cast<const IO*>(gate), init, static_cast<IO*>(y), final_state, states);
 }
 
-// Tokens that one thread walks rather than a cluster: a warp's tile, behind which the other warps would idle.
-constexpr int64_t kShort = 16;
+// Whether single threads walk the sequences.  That takes 0.1 us a token whatever the batch is, and a chain 7 ns a column
+// to begin with, so it pays for few tokens and for many columns (us, threads against the other kernels, bf16: 64 x 5120
+// channels, 16 tokens 6.4 and 39, 256 tokens 89 and 112, 512 tokens 175 and 186; 16 x 5120, 64 tokens 13.5 and 14.8, 128
+// tokens 26 and 20; 4 x 1536, 8 tokens 1.7 and 1.9, 16 tokens 2.3 and 1.9).  float32 has half the tokens in flight.
+bool by_threads(const GatedProblem& p) {
+  const int64_t columns = columns64(p) * p.b, room = columns / 8;
+  return p.L * (p.io_bf16 ? 2 : 4) <= (room < 16 ? 16 : room);
+}
 
 // Columns of 64 channels, over the whole batch, below which even clusters of eight CTAs leave SMs without work: then segments,
-// if the sequence is long enough to be worth a second reading (65536 tokens, 8 columns, float32: 104 us).  With more
-// columns than SMs each column of 32 has a chain of its own.
+// if the sequence is long enough to be worth a second reading (65536 tokens, segments against clusters: 4 columns, bf16, 36
+// and 146 us; 16 columns 123 and 186; 32 columns 236 and 195; 16 columns of 4096 tokens 13.6 and 13.7).  With more columns
+// than SMs each column of 32 has a chain of its own (chains against clusters: 8192 tokens, 160 columns, 113 and 121
+// us, float32 164 and 200; 320 columns 188 and 236; 152 columns 107 and 95).
 bool in_segments(const GatedProblem& p) {
   return columns64(p) * p.b < 24 && p.L >= 32 * kMapWarps * (p.io_bf16 ? kTokens<uint16_t> : kTokens<float>);
 }
@@ -457,7 +469,7 @@ size_t gated_workspace_bytes(const GatedProblem& p) {
 cudaError_t launch_gated_scan(const GatedProblem& p, const void* x, const void* gate, const float* init, void* y,
                               float* final_state, float* states, void* ws, cudaStream_t st) {
   using namespace gated;
-  if (p.L <= kShort) return run(p, x, gate, init, y, final_state, states, st);
+  if (by_threads(p)) return run(p, x, gate, init, y, final_state, states, st);
   const Maps maps{static_cast<float*>(ws), columns64(p) * kCols};
   return with_types(p, piece_bytes(p, x, gate), [&](auto io, auto g, auto kind, auto comp) {
     using IO = decltype(io);

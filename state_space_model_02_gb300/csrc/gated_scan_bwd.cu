@@ -9,6 +9,11 @@
 // block, so only the adjoint is carried between CTAs and steps; inside a tile each warp reduces its tokens to
 // (P, H, R), walks the states forward from the one that enters its tokens and the adjoint backward from the one that
 // leaves them.  x, gate and dy are read once, dx and dgate written once.
+//
+// Bound by instructions (51 a value; bf16 b2 L8192 D5120: 51% of the issue slots, DRAM 44% busy) and the one barrier a step.
+// b2 L8192 D5120 233 us with bf16 (53% of the measured copy bandwidth), 304 us with float32 (82%).  With an extra warp that
+// exchanges the maps, as the forward pass has it, the best of its shapes took 253 us against 223 without (both with
+// the decays straight from the MUFU unit): it takes registers that the 8 tokens of four arrays need.
 #include "gated.cuh"
 
 namespace ssd {
@@ -139,7 +144,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(
     float2 q;  // what the tokens right of this warp's send to its last state
     if (K > 1) {
       if (w == 0) {
-        publish_map<true, kWarps>(cta_map, warp_map[par], rank, K, lane);
+        publish_map(cta_map, warp_map[par], rank, K, lane);
         cluster_arrive();
       } else {
         cluster_arrive_relaxed();
@@ -278,8 +283,13 @@ __global__ void __launch_bounds__(kWarps * 32) map_bwd_kernel(const Args p, cons
 }
 
 // Few columns leave SMs without work even in clusters: then segments, if the sequence is long enough to be worth a second
-// reading.
-bool in_segments(const GatedProblem& p) { return columns64(p) * p.b < 24 && p.L >= 32 * SSD_GATED_BLOCK; }
+// reading of gate and dy.  (Segments against clusters, bf16, us: 24 columns, 2048 tokens 13.6 and 13.8, 32768 tokens 134 and
+// 188; 32 columns, 2048 tokens 16.5 and 14.3, 8192 tokens 51 and 51, 32768 tokens 172 and 197; 47 columns, 8192 tokens
+// 72 and 77, 32768 tokens 253 and 298; 64 columns, 8192 tokens 99 and 94, with float32 142 and 119.)
+bool in_segments(const GatedProblem& p) {
+  const int64_t columns = columns64(p) * p.b;
+  return columns < 48 && p.L >= (columns <= 24 ? 32 : 128) * SSD_GATED_BLOCK;
+}
 Plan bwd_segments(const GatedProblem& p) {
   return segment_plan(p, columns64(p), SSD_GATED_BLOCK, int64_t(kResident) * kSMs / (columns64(p) * p.b), SSD_GATED_BLOCK);
 }

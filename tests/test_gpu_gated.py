@@ -126,6 +126,23 @@ def test_larger(b, L, D, dtype):
     check_backward(t, check_forward(t, dtype, "logit", True), dtype, "logit", True)
 
 
+@pytest.mark.parametrize("b,L,D,dtype", [(1, 8, 130, "bf16"), (1, 9, 130, "bf16"), (1, 4, 130, "f32"), (1, 5, 130, "f32"),
+                                         (64, 130, 2050, "bf16"), (64, 132, 2048, "bf16"), (64, 65, 2048, "f32"),
+                                         (80, 63, 1001, "f32"), (2, 20, 9216, "bf16"), (2, 19, 9216, "bf16")])
+def test_short_sequences(b, L, D, dtype):
+    """On both sides of what single threads walk: few tokens, or many columns with blocks of 64 tokens to save."""
+    t = inputs(b, L, D, dtype, "logit", seed=b + L + D)
+    check_backward(t, check_forward(t, dtype, "logit", True), dtype, "logit", True)
+
+
+@pytest.mark.parametrize("L,D,dtype", [(8192, 1600, "bf16"), (8193, 3008, "bf16"), (8191, 1601, "f32"), (8200, 1601, "f32"),
+                                       (2048, 1536, "bf16"), (8192, 3009, "f32")])
+def test_columns_in_segments_and_clusters(L, D, dtype):
+    """On both sides of the columns and lengths that the backward pass cuts into segments."""
+    t = inputs(1, L, D, dtype, "log", seed=L + D)
+    check_backward(t, check_forward(t, dtype, "log", False), dtype, "log", False)
+
+
 def test_no_initial_state_and_no_dfinal():
     t = inputs(2, 200, 48, "f32", "logit", 7, init=False)
     check_backward(t, check_forward(t, "f32", "logit", False), "f32", "logit", False, dfinal=False)
