@@ -85,7 +85,7 @@ __device__ __forceinline__ float exp_of(float g) {
 // The decay a and s = 1 - a, to a rounding of float32 near a = 1 each: a state of long memory adds up a thousand times what
 // its decay is off by, and there the MUFU unit's results, good to two units or so, would cost digits: the last state of
 // 256K tokens, decay exp(gate), differs from float64 by 1.9e-6 (rms, relative) with them, by 2.0e-7 without, and by 3.2e-7
-// in a plain float32 scan.  It costs the scan up to 13% (32768 x 2048: 82.5 -> 93.1 us).  s is taken from the gate, not
+// in a plain float32 scan.  It costs the scan up to 14% (262144 x 2048: 626 -> 714 us).  s is taken from the gate, not
 // from a: near a = 1 the difference has lost its low bits.
 // 1 - exp(g) = -g q(g): for small |g| q is a series (the first term left out is g^6 / 5040 of it, under 5e-8).
 constexpr float kSmallGate = 0.25f;
