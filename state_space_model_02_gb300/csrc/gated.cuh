@@ -150,11 +150,16 @@ __device__ __forceinline__ void gate_of(float2 g, float2& a, float2& s) {
 
 // A warp's tile of one tensor: TW tokens of a column of COLS channels, in shared memory row after row.  It is copied in
 // and out in pieces of G bytes, neighbouring lanes neighbouring pieces: 16 where every row starts at a multiple of
-// 16 bytes, else 4, and 2 for bf16 rows that start between two words.  Pieces behind token `end` or channel D are zeros.
-// A lane has two channels of a column of 64, or one of 32.
+// 16 bytes, else 4.  Pieces behind token `end` or channel D are zeros.  A lane has two channels of a column of 64, or one of
+// 32.  G = 2 are bf16 rows that start between two words: they are copied in 16 bytes from the multiple of 16 before their
+// start on, up to their end and no further, into rows with 16 bytes more; a reader adds what its row starts behind that
+// multiple.  Copies of two bytes do not exist; loads and stores to shared memory in their place are waited for (2 x 138977
+// tokens of 307 channels 1446 us, 295 so; backward 4 x 2579 x 2623 274 and 155).  Where rows start at multiples of 4, pieces
+// of 4 are faster, which need no shift: 4 x 2048 x 1538 33 against 46 us, backward 4 x 2579 x 2622 104 against 154.
 template <typename IO, int G, int TW, int COLS>
 struct Tile {
-  static constexpr int kBytes = TW * COLS * int(sizeof(IO));
+  static constexpr int kRow = COLS * int(sizeof(IO)) + (G == 2 ? 16 : 0);  // bytes of a row that is copied in
+  static constexpr int kBytes = TW * kRow;
   static constexpr int kPerRow = COLS * int(sizeof(IO)) / G;
   static constexpr int kPieces = TW * kPerRow / 32;  // a lane's
 
@@ -174,26 +179,62 @@ struct Tile {
       asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(from), "r"(bytes) : "memory");
   }
 
-  // src: the column's first channel in token 0 of this batch; left: channels of the column inside the tensor
-  static __device__ __forceinline__ void in(char* tile, const IO* src, int64_t stride, int64_t t0, int64_t end, int left,
-                                            int lane) {
-    if constexpr (G == 2) {  // IO is bf16
-      constexpr int kBatch = 8, kEach = COLS / 32;  // tokens whose values are on their way at once, channels of a lane
-      const int ch = kEach * lane;
-#pragma unroll
-      for (int i0 = 0; i0 < TW; i0 += kBatch) {
-        uint32_t r[kBatch];
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const uint16_t* row = reinterpret_cast<const uint16_t*>(src) + (t0 + i0 + i) * stride + ch;
-          const bool in = t0 + i0 + i < end;
-          r[i] = in && ch < left ? __ldg(row) : 0;
-          if (kEach == 2 && in && ch + 1 < left) r[i] |= uint32_t(__ldg(row + 1)) << 16;
+  static __device__ __forceinline__ void copy16(uint32_t dst, uintptr_t from, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(bytes) : "memory");
+  }
+
+  // What a lane reads of a tile that was copied in: the values of token t0 + i.
+  struct Reader {
+    const char* at;
+    uint32_t off, step;  // bytes that row 0 starts behind a multiple of 16, and every further one more
+    __device__ __forceinline__ auto operator[](int i) const {
+      if constexpr (G == 2) {
+        const uint32_t o = (off + i * step) & 15;
+        if constexpr (COLS == 32) {
+          return widen(*reinterpret_cast<const uint16_t*>(at + i * kRow + o));
+        } else {
+          const uint32_t* word = reinterpret_cast<const uint32_t*>(at + i * kRow + (o & 12));
+          return widen(__funnelshift_r(word[0], word[1], (o & 2) * 8));
         }
-        using lane_t = std::conditional_t<kEach == 2, uint32_t, uint16_t>;
+      } else if constexpr (COLS == 32) {
+        return widen(*reinterpret_cast<const IO*>(at + i * kRow));
+      } else {
+        return widen(*reinterpret_cast<const pair_t<IO>*>(at + i * kRow));
+      }
+    }
+  };
+  static __device__ __forceinline__ Reader reader(const char* tile, const IO* src, int64_t stride, int64_t t0, int lane) {
+    Reader r{tile + lane * (COLS / 32) * int(sizeof(IO)), 0, 0};
+    if constexpr (G == 2) {
+      r.step = static_cast<uint32_t>(stride * 2) & 15;
+      r.off = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(src + t0 * stride)) & 15;
+    }
+    return r;
+  }
+
+  // src: the column's first channel in token 0 of this batch; left: channels of the column inside the tensor, which
+  // starts at `first`
+  static __device__ __forceinline__ void in(char* tile, const IO* src, int64_t stride, int64_t t0, int64_t end, int left,
+                                            int lane, const IO* first) {
+    if constexpr (G == 2) {
+      constexpr int kPer = kRow / 16, kAll = TW * kPer;
+      const uint32_t dst = smem_u32(tile);
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-          reinterpret_cast<lane_t*>(tile)[(i0 + i) * 32 + lane] = static_cast<lane_t>(r[i]);
+      for (int j = 0; j < (kAll + 31) / 32; ++j) {
+        const int k = 32 * j + lane, row = k / kPer;
+        if (k >= kAll) break;
+        const uintptr_t at = reinterpret_cast<uintptr_t>(src + (t0 + row) * stride), stop = at + 2 * left;
+        const uintptr_t from = (at & ~uintptr_t(15)) + 16 * (k - row * kPer);
+        const bool ok = t0 + row < end && from < stop;
+        const int bytes = !ok ? 0 : stop - from < 16 ? int(stop - from) : 16;
+        if (ok && from < reinterpret_cast<uintptr_t>(first)) {  // the tensor's first row: nothing before it is read
+          uint16_t* to = reinterpret_cast<uint16_t*>(tile) + 8 * k;
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i)
+            to[i] = from + 2 * i >= at && 2 * i < bytes ? *reinterpret_cast<const uint16_t*>(from + 2 * i) : uint16_t(0);
+        } else {
+          copy16(dst + 16 * k, ok ? from : at & ~uintptr_t(15), bytes);
+        }
       }
     } else if (t0 + TW <= end && left == COLS) {  // nothing to leave out
       const uint32_t dst = smem_u32(tile) + lane * G;

@@ -124,8 +124,8 @@ __global__ void __launch_bounds__((NW + 1) * 32, kResident) scan_kernel(
   auto fetch = [&](int slot, int64_t t) {
     char* s = slots + slot * (2 * T::kBytes);
     if (t < p.L) {
-      T::in(s, xb, p.sx, t, p.L, left, lane);
-      T::in(s + T::kBytes, gb, p.sg, t, p.L, left, lane);
+      T::in(s, xb, p.sx, t, p.L, left, lane, x);
+      T::in(s + T::kBytes, gb, p.sg, t, p.L, left, lane, gate);
     }
     copies_commit();
   };
@@ -134,15 +134,15 @@ __global__ void __launch_bounds__((NW + 1) * 32, kResident) scan_kernel(
 
   int slot = 0;
   for (int step = 0; step < p.steps; ++step) {
-    pair_t<IO>* xs = reinterpret_cast<pair_t<IO>*>(slots + slot * (2 * T::kBytes)) + lane;
-    const pair_t<IO>* gs = reinterpret_cast<const pair_t<IO>*>(slots + slot * (2 * T::kBytes) + T::kBytes) + lane;
+    char* tile = slots + slot * (2 * T::kBytes);
+    const auto xs = T::reader(tile, xb, p.sx, t0, lane), gs = T::reader(tile + T::kBytes, gb, p.sg, t0, lane);
     copies_wait<NS - 1>();
     __syncwarp();
     float2 a[TW], u[TW], s, P = make_float2(1.f, 1.f), H = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < TW; ++i) {
-      gate_of<IO, KIND, false>(widen(gs[i * 32]), a[i], s);
-      u[i] = widen(xs[i * 32]);
+      gate_of<IO, KIND, false>(gs[i], a[i], s);
+      u[i] = xs[i];
       if constexpr (COMP) u[i] = mul_f32x2(u[i], s);
       H = chain_fma(a[i], H, u[i]);
       P = chain_mul(P, a[i]);
@@ -154,24 +154,25 @@ __global__ void __launch_bounds__((NW + 1) * 32, kResident) scan_kernel(
     cluster_wait();
     named_bar_sync(2, (NW + 1) * 32);
     float2 h = entering[w][lane];
+    pair_t<IO>* ys = reinterpret_cast<pair_t<IO>*>(tile) + lane;  // x has been read by all lanes: y leaves from its place
     if (states && t0 % SSD_GATED_BLOCK == 0 && t0 < p.L)
       store_row(states + (b * blocks + t0 / SSD_GATED_BLOCK) * p.D, c, p.D, h);
     if (final_state && t0 < p.L && p.L <= t0 + TW) {  // the last token is one of this warp's
 #pragma unroll
       for (int i = 0; i < TW; ++i) {
         h = chain_fma(a[i], h, u[i]);
-        narrow(xs[i * 32], h);
+        narrow(ys[i * 32], h);
         if (t0 + i == p.L - 1) store_row(final_state + b * p.D, c, p.D, h);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < TW; ++i) {
         h = chain_fma(a[i], h, u[i]);
-        narrow(xs[i * 32], h);  // x has been read: y leaves from its place
+        narrow(ys[i * 32], h);
       }
     }
     __syncwarp();
-    T::out(reinterpret_cast<const char*>(xs - lane), yb, p.D, t0, p.L, left, lane);
+    T::out(tile, yb, p.D, t0, p.L, left, lane);
     __syncwarp();
     fetch(slot, t0 + NS * span);
     t0 += span;
@@ -210,8 +211,8 @@ __global__ void __launch_bounds__(NW * 32, kChainResident) chain_kernel(
   auto fetch = [&](int slot, int64_t t) {
     char* s = slots + slot * (2 * T::kBytes);
     if (t < end) {
-      T::in(s, xb, p.sx, t, end, left, lane);
-      T::in(s + T::kBytes, gb, p.sg, t, end, left, lane);
+      T::in(s, xb, p.sx, t, end, left, lane, x);
+      T::in(s + T::kBytes, gb, p.sg, t, end, left, lane, gate);
     }
     copies_commit();
   };
@@ -241,15 +242,15 @@ __global__ void __launch_bounds__(NW * 32, kChainResident) chain_kernel(
 
   int slot = 0;
   for (; t0 < end; t0 += NW * TW) {
-    const IO* xs = reinterpret_cast<const IO*>(slots + slot * (2 * T::kBytes)) + lane;
-    const IO* gs = reinterpret_cast<const IO*>(slots + slot * (2 * T::kBytes) + T::kBytes) + lane;
+    const char* tile = slots + slot * (2 * T::kBytes);
+    const auto xs = T::reader(tile, xb, p.sx, t0, lane), gs = T::reader(tile + T::kBytes, gb, p.sg, t0, lane);
     copies_wait<NS - 1>();
     __syncwarp();
     float2 a[TW / 2], u[TW / 2], s;  // of two tokens
 #pragma unroll
     for (int i = 0; i < TW / 2; ++i) {
-      gate_of<IO, KIND, false>(make_float2(widen(gs[i * 64]), widen(gs[i * 64 + 32])), a[i], s);
-      u[i] = make_float2(widen(xs[i * 64]), widen(xs[i * 64 + 32]));
+      gate_of<IO, KIND, false>(make_float2(gs[2 * i], gs[2 * i + 1]), a[i], s);
+      u[i] = make_float2(xs[2 * i], xs[2 * i + 1]);
       if constexpr (COMP) u[i] = mul_f32x2(u[i], s);
     }
     __syncwarp();
@@ -309,8 +310,8 @@ __global__ void __launch_bounds__(NW * 32) map_kernel(const Args p, const IO* __
     auto fetch = [&](int slot, int64_t t) {
       char* s = slots + slot * (2 * T::kBytes);
       if (t < end) {
-        T::in(s, xb, p.sx, t, end, left, lane);
-        T::in(s + T::kBytes, gb, p.sg, t, end, left, lane);
+        T::in(s, xb, p.sx, t, end, left, lane, x);
+        T::in(s + T::kBytes, gb, p.sg, t, end, left, lane, gate);
       }
       copies_commit();
     };
@@ -318,14 +319,14 @@ __global__ void __launch_bounds__(NW * 32) map_kernel(const Args p, const IO* __
     for (int k = 0; k < NS; ++k) fetch(k, t0 + k * TW);
     int slot = 0;
     for (int64_t t = t0; t < end; t += TW) {  // seg_len is a multiple of the eight warps' tiles
-      const pair_t<IO>* xs = reinterpret_cast<const pair_t<IO>*>(slots + slot * (2 * T::kBytes)) + lane;
-      const pair_t<IO>* gs = reinterpret_cast<const pair_t<IO>*>(slots + slot * (2 * T::kBytes) + T::kBytes) + lane;
+      const char* tile = slots + slot * (2 * T::kBytes);
+      const auto xs = T::reader(tile, xb, p.sx, t, lane), gs = T::reader(tile + T::kBytes, gb, p.sg, t, lane);
       copies_wait<NS - 1>();
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < TW; ++i) {
-        float2 a, s, u = widen(xs[i * 32]);
-        gate_of<IO, KIND, false>(widen(gs[i * 32]), a, s);
+        float2 a, s, u = xs[i];
+        gate_of<IO, KIND, false>(gs[i], a, s);
         if constexpr (COMP) u = mul_f32x2(u, s);
         H = chain_fma(a, H, u);
         P = chain_mul(P, a);

@@ -75,9 +75,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(
   auto fetch = [&](int slot, int64_t t) {
     char* s = slots + slot * kSlot;
     if (t >= start) {
-      T::in(s, xb, p.sx, t, end, left, lane);
-      T::in(s + T::kBytes, gb, p.sg, t, end, left, lane);
-      T::in(s + 2 * T::kBytes, db, p.D, t, end, left, lane);
+      T::in(s, xb, p.sx, t, end, left, lane, x);
+      T::in(s + T::kBytes, gb, p.sg, t, end, left, lane, gate);
+      T::in(s + 2 * T::kBytes, db, p.D, t, end, left, lane, dy);
     }
     copies_commit();
   };
@@ -113,9 +113,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(
     char* sl = slots + slot * kSlot;
     char* stage = kStaged<IO> ? slots + NS * kSlot : sl;
     float2(*cta_map)[2][32] = cta_maps + par * K;
-    const pair_t<IO>* xs = reinterpret_cast<const pair_t<IO>*>(sl) + lane;
-    const pair_t<IO>* gs = reinterpret_cast<const pair_t<IO>*>(sl + T::kBytes) + lane;
-    const pair_t<IO>* ds = reinterpret_cast<const pair_t<IO>*>(sl + 2 * T::kBytes) + lane;
+    const auto xs = T::reader(sl, xb, p.sx, t0, lane), gs = T::reader(sl + T::kBytes, gb, p.sg, t0, lane);
+    const auto ds = T::reader(sl + 2 * T::kBytes, db, p.D, t0, lane);
     float2 h = next_state;
     next_state = state_of(t0 - span);
     copies_wait<NS - 1>();
@@ -124,9 +123,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) scan_bwd_kernel(
     float2 P = make_float2(1.f, 1.f), H = make_float2(0.f, 0.f), R = make_float2(0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < kTok; ++i) {
-      gate_of<IO, KIND, true>(widen(gs[i * 32]), a[i], s[i]);
-      xv[i] = widen(xs[i * 32]);
-      d[i] = widen(ds[i * 32]);
+      gate_of<IO, KIND, true>(gs[i], a[i], s[i]);
+      xv[i] = xs[i];
+      d[i] = ds[i];
       H = chain_fma(a[i], H, COMP ? mul_f32x2(xv[i], s[i]) : xv[i]);
     }
     add_final(d, dfinal, t0, p, b, c);
@@ -238,23 +237,23 @@ __global__ void __launch_bounds__(kWarps * 32) map_bwd_kernel(const Args p, cons
   if (seg > 0) {  // no segment is before the first one
     auto fetch = [&](int slot, int64_t t) {
       char* s = slots + slot * (2 * T::kBytes);
-      T::in(s, gb, p.sg, t, end, left, lane);
-      T::in(s + T::kBytes, db, p.D, t, end, left, lane);
+      T::in(s, gb, p.sg, t, end, left, lane, gate);
+      T::in(s + T::kBytes, db, p.D, t, end, left, lane, dy);
       copies_commit();
     };
 #pragma unroll
     for (int k = 0; k < NS; ++k) fetch(k, t0 + k * kTok);
     int slot = 0;
     for (int64_t t = t0; t < end; t += kTok) {
-      const pair_t<IO>* gs = reinterpret_cast<const pair_t<IO>*>(slots + slot * (2 * T::kBytes)) + lane;
-      const pair_t<IO>* ds = reinterpret_cast<const pair_t<IO>*>(slots + slot * (2 * T::kBytes) + T::kBytes) + lane;
+      const char* tile = slots + slot * (2 * T::kBytes);
+      const auto gs = T::reader(tile, gb, p.sg, t, lane), ds = T::reader(tile + T::kBytes, db, p.D, t, lane);
       copies_wait<NS - 1>();
       __syncwarp();
       float2 d[kTok], a[kTok], s;
 #pragma unroll
       for (int i = 0; i < kTok; ++i) {
-        gate_of<IO, KIND, true>(widen(gs[i * 32]), a[i], s);
-        d[i] = widen(ds[i * 32]);
+        gate_of<IO, KIND, true>(gs[i], a[i], s);
+        d[i] = ds[i];
       }
       add_final(d, dfinal, t, p, b, c);
 #pragma unroll

@@ -143,6 +143,18 @@ def test_columns_in_segments_and_clusters(L, D, dtype):
     check_backward(t, check_forward(t, dtype, "log", False), dtype, "log", False)
 
 
+@pytest.mark.parametrize("b,L,D", [(1, 6000, 123), (2, 2600, 1001), (11, 257, 1001), (1, 40, 1), (3, 70, 65), (5, 200, 4097)])
+@pytest.mark.parametrize("at,more", [(0, 0), (1, 2), (33, 40), (7, 9)])
+def test_odd_rows(b, L, D, at, more):
+    """bf16 rows at every offset from a multiple of 16 bytes, in each kernel; what lies around them is never taken in."""
+    t = inputs(b, L, D, "bf16", "logit", seed=L + D + at)
+    for k in ("x", "gate"):
+        wide = torch.full((b, L, D + more), float("nan"), dtype=torch.bfloat16, device="cuda")
+        wide[:, :, at:at + D] = t[k]
+        t[k] = wide[:, :, at:at + D]
+    check_backward(t, check_forward(t, "bf16", "logit", True), "bf16", "logit", True)
+
+
 def test_no_initial_state_and_no_dfinal():
     t = inputs(2, 200, 48, "f32", "logit", 7, init=False)
     check_backward(t, check_forward(t, "f32", "logit", False), "f32", "logit", False, dfinal=False)
