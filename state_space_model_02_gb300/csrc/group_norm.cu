@@ -26,7 +26,7 @@ namespace {
 // (16384 x 5120 in one group, bf16, silu: 70 us, 71% of the measured copy bandwidth; with copies ahead 81 us).
 // 16384 x 5120 in 8 groups, gate_first: 88 us (84%).  HBM is 76% busy, the MUFU unit 41%.
 template <typename IO, int VEC, int ACT, int R, int LANES>
-__global__ void __launch_bounds__(LANES ? 256 : 512, LANES ? 1 : 2) row_kernel(const NormProblem p, int stride, const IO* __restrict__ x,
+__global__ void __launch_bounds__(LANES ? 256 : 512, LANES || R > 4 ? 1 : 2) row_kernel(const NormProblem p, int stride, const IO* __restrict__ x,
                                                                 const IO* __restrict__ z, const float* __restrict__ w,
                                                                 const float* __restrict__ bias, IO* __restrict__ y,
                                                                 float* __restrict__ mean, float* __restrict__ rstd) {
@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(LANES ? 256 : 512, LANES ? 1 : 2) row_kernel(c
   extern __shared__ __align__(16) char ring[];
   __shared__ float part[2][2][32];
   const int threads = blockDim.x, lanes = LANES ? LANES : threads, l = LANES ? threadIdx.x % LANES : threadIdx.x;
-  typename P::raw* slots = reinterpret_cast<typename P::raw*>(ring) + threadIdx.x;
+  typename P::slot* slots = reinterpret_cast<typename P::slot*>(ring) + threadIdx.x;
   const int Cg = static_cast<int>(p.C / p.G);
   const uint32_t team = LANES ? blockIdx.x * (threads / LANES) + threadIdx.x / LANES : blockIdx.x, groups = p.G;
   const int64_t g = team % groups, first = team / groups;
@@ -61,12 +61,12 @@ __global__ void __launch_bounds__(LANES ? 256 : 512, LANES ? 1 : 2) row_kernel(c
   }
   grid_dep_wait();
   auto fetch = [&](int slot, int64_t n) {
-    typename P::raw* to = slots + slot * (R * kTensors) * threads;
+    typename P::slot* to = slots + slot * (R * kTensors) * threads;
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       if (mine[k] && n < p.n) {
-        P::copy(to + k * kTensors * threads, xp + k * lanes * VEC);
-        if constexpr (kGated) P::copy(to + (k * kTensors + 1) * threads, zp + k * lanes * VEC);
+        P::copy(to + k * kTensors * threads, xp + k * lanes * VEC, x);
+        if constexpr (kGated) P::copy(to + (k * kTensors + 1) * threads, zp + k * lanes * VEC, z);
       }
     }
     copies_commit();
@@ -83,11 +83,11 @@ __global__ void __launch_bounds__(LANES ? 256 : 512, LANES ? 1 : 2) row_kernel(c
     P xr[R], zr[kGated ? R : 1];
     if constexpr (kRing) {
       copies_wait<kSlots - 1>();
-      const typename P::raw* at = slots + slot * (R * kTensors) * threads;
+      const typename P::slot* at = slots + slot * (R * kTensors) * threads;
 #pragma unroll
       for (int k = 0; k < R; ++k) {
-        xr[k].r = at[k * kTensors * threads];
-        if constexpr (kGated) zr[k].r = at[(k * kTensors + 1) * threads];
+        xr[k].take(at[k * kTensors * threads], x + n * p.sx + c0 + k * lanes * VEC);
+        if constexpr (kGated) zr[k].take(at[(k * kTensors + 1) * threads], z + n * p.sz + c0 + k * lanes * VEC);
       }
       fetch(slot, n + kSlots * stride);
       slot = slot + 1 == kSlots ? 0 : slot + 1;
@@ -149,9 +149,13 @@ __global__ void __launch_bounds__(LANES ? 256 : 512, LANES ? 1 : 2) row_kernel(c
   grid_dep_launch();
 }
 
-// Packs of a group that a CTA of 512 threads holds
-constexpr int kMostPacks = 2048;
-bool rows_ok(const NormProblem& p, int vec) { return p.S == 1 && p.C / p.G / vec <= kMostPacks; }
+// Packs of `bytes` that a thread's registers hold: 64 bytes of a tensor, and no more than 16.  512 threads hold a group of 8192
+// channels whatever its rows' alignment is, 16384 of bf16 in packs of 16 bytes; a wider one is read twice, in tiles of
+// one position each.  (10048 samples of 2057 float32 channels: 1077 us in tiles, 55 so.)
+constexpr int most_packs(int bytes) { return bytes < 4 ? 16 : 64 / bytes; }
+bool rows_ok(const NormProblem& p, int vec) {
+  return p.S == 1 && p.C / p.G / vec <= 512 * most_packs(vec * (p.io_bf16 ? 2 : 4));
+}
 
 template <typename IO, int VEC, int ACT, int R, int LANES>
 cudaError_t launch_rows(const NormProblem& p, int threads, const IO* x, const IO* z, const float* w, const float* b, IO* y,
@@ -160,7 +164,7 @@ cudaError_t launch_rows(const NormProblem& p, int threads, const IO* x, const IO
   int64_t stride = p.n, per_cta = 1;
   size_t smem = 0;
   if constexpr (LANES != 0) {
-    smem = size_t(threads) * R * (ACT == SSD_NORM_GATE || ACT == SSD_NORM_GATE_FIRST ? 2 : 1) * kRowSlots * Pack<IO, VEC>::kBytes;
+    smem = size_t(threads) * R * (ACT == SSD_NORM_GATE || ACT == SSD_NORM_GATE_FIRST ? 2 : 1) * kRowSlots * Pack<IO, VEC>::kSlotBytes;
     cudaError_t e = allow_smem<row_kernel<IO, VEC, ACT, R, LANES>>(int(smem));
     if (e != cudaSuccess) return e;
     static OncePerDevice<> known;  // CTAs that an SM holds
@@ -195,7 +199,15 @@ cudaError_t rows(const NormProblem& p, const IO* x, const IO* z, const float* w,
   if (items <= 64) return launch_rows<IO, VEC, ACT, 2, 32>(p, 256, x, z, w, b, y, mean, rstd, st);
   if (items <= 96) return launch_rows<IO, VEC, ACT, 3, 32>(p, 256, x, z, w, b, y, mean, rstd, st);
   if (items <= 256) return launch_rows<IO, VEC, ACT, 2, 0>(p, round_up(ceil_div(items, 2), 32), x, z, w, b, y, mean, rstd, st);
-  return launch_rows<IO, VEC, ACT, 4, 0>(p, round_up(ceil_div(items, 4), 32), x, z, w, b, y, mean, rstd, st);
+  constexpr int kMost = most_packs(Pack<IO, VEC>::kBytes);
+  if (items <= 2048) return launch_rows<IO, VEC, ACT, 4, 0>(p, round_up(ceil_div(items, 4), 32), x, z, w, b, y, mean, rstd, st);
+  if constexpr (kMost >= 8) {
+    if (items <= 4096) return launch_rows<IO, VEC, ACT, 8, 0>(p, round_up(ceil_div(items, 8), 32), x, z, w, b, y, mean, rstd, st);
+  }
+  if constexpr (kMost >= 16) {
+    if (items <= 8192) return launch_rows<IO, VEC, ACT, 16, 0>(p, round_up(ceil_div(items, 16), 32), x, z, w, b, y, mean, rstd, st);
+  }
+  return cudaErrorInvalidConfiguration;  // rows_ok lets no larger group through
 }
 
 // ------------------------------------------------------------------------------ tiles

@@ -93,18 +93,34 @@ struct Pack {
   static constexpr int kBytes = VEC * int(sizeof(IO));
   using raw = std::conditional_t<kBytes == 16, uint4, std::conditional_t<kBytes == 8, uint2, std::conditional_t<kBytes == 4, uint32_t, uint16_t>>>;
   raw r;
+  // what holds a copied pack in shared memory: of a single bf16 value the word that it lies in
+  using slot = std::conditional_t<kBytes == 2, uint32_t, raw>;
+  static constexpr int kSlotBytes = sizeof(slot);
 
   __device__ __forceinline__ void load(const IO* p) { r = __ldg(reinterpret_cast<const raw*>(p)); }
-  // An asynchronous copy of a pack to shared memory (of single bf16 values, which it does not take, a plain one).
-  static __device__ __forceinline__ void copy(raw* to, const IO* from) {
+  // An asynchronous copy of a pack of the tensor that starts at `first` to shared memory.  Two bytes it does not take: the
+  // word around them, where all of that is in the tensor, of which nothing behind the value is read.
+  static __device__ __forceinline__ void copy(slot* to, const IO* from, const IO* first) {
     if constexpr (kBytes == 16)
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
     else if constexpr (kBytes == 8)
       asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(to)), "l"(from) : "memory");
     else if constexpr (kBytes == 4)
       asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+    else {
+      const uintptr_t at = reinterpret_cast<uintptr_t>(from), odd = at & 2, word = at - odd;
+      if (word < reinterpret_cast<uintptr_t>(first))
+        *to = uint32_t(__ldg(reinterpret_cast<const raw*>(from))) << 16;
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(to)), "l"(word), "r"(2 + int(odd)) : "memory");
+    }
+  }
+  // The pack that was copied from there
+  __device__ __forceinline__ void take(slot s, const IO* from) {
+    if constexpr (kBytes == 2)
+      r = static_cast<raw>(reinterpret_cast<uintptr_t>(from) & 2 ? s >> 16 : s);
     else
-      *to = __ldg(reinterpret_cast<const raw*>(from));
+      r = s;
   }
   __device__ __forceinline__ void store(IO* p) const { *reinterpret_cast<raw*>(p) = r; }
   __device__ __forceinline__ Vals<VEC> widen() const {

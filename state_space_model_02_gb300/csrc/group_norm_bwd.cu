@@ -48,18 +48,21 @@ struct Back {
 
 // ------------------------------------------------------------------------------ rows
 
+// Samples that a thread has on their way or at hand: fewer where `bytes` a tensor of them would not fit
+constexpr int row_slots(int bytes) { return bytes > 32 ? 2 : kRowSlots; }
+
 template <typename IO, int VEC, int ACT, int R, int LANES>
 __global__ void __launch_bounds__(LANES ? 256 : 512) row_bwd_kernel(
     const NormProblem p, int stride, const IO* __restrict__ x, const IO* __restrict__ z, const float* __restrict__ w,
     const float* __restrict__ bias, const IO* __restrict__ dy, const float* __restrict__ mean,
     const float* __restrict__ rstd, IO* __restrict__ dx, IO* __restrict__ dz, float* __restrict__ shares) {
   constexpr bool kGated = ACT == SSD_NORM_GATE || ACT == SSD_NORM_GATE_FIRST;
-  constexpr int kTensors = kGated ? 3 : 2, kSlots = kRowSlots;
+  constexpr int kTensors = kGated ? 3 : 2, kSlots = row_slots(R * Pack<IO, VEC>::kSlotBytes);
   using P = Pack<IO, VEC>;
   extern __shared__ __align__(16) char ring[];
   __shared__ float part[2][2][32];
   const int threads = blockDim.x, lanes = LANES ? LANES : threads, l = LANES ? threadIdx.x % LANES : threadIdx.x;
-  typename P::raw* slots = reinterpret_cast<typename P::raw*>(ring) + threadIdx.x;
+  typename P::slot* slots = reinterpret_cast<typename P::slot*>(ring) + threadIdx.x;
   const int Cg = static_cast<int>(p.C / p.G);
   const uint32_t team = LANES ? blockIdx.x * (threads / LANES) + threadIdx.x / LANES : blockIdx.x, groups = p.G;
   const int64_t g = team % groups, first = team / groups;
@@ -74,13 +77,13 @@ __global__ void __launch_bounds__(LANES ? 256 : 512) row_bwd_kernel(
   const IO* dp = dy + first * p.C + c0;
   grid_dep_wait();
   auto fetch = [&](int slot, int64_t n) {
-    typename P::raw* to = slots + slot * (R * kTensors) * threads;
+    typename P::slot* to = slots + slot * (R * kTensors) * threads;
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       if (mine[k] && n < p.n) {
-        P::copy(to + k * kTensors * threads, xp + k * lanes * VEC);
-        P::copy(to + (k * kTensors + 1) * threads, dp + k * lanes * VEC);
-        if constexpr (kGated) P::copy(to + (k * kTensors + 2) * threads, zp + k * lanes * VEC);
+        P::copy(to + k * kTensors * threads, xp + k * lanes * VEC, x);
+        P::copy(to + (k * kTensors + 1) * threads, dp + k * lanes * VEC, dy);
+        if constexpr (kGated) P::copy(to + (k * kTensors + 2) * threads, zp + k * lanes * VEC, z);
       }
     }
     copies_commit();
@@ -104,7 +107,7 @@ __global__ void __launch_bounds__(LANES ? 256 : 512) row_bwd_kernel(
     const float2 st = next;
     next = stat(n + stride);
     copies_wait<kSlots - 1>();
-    const typename P::raw* at = slots + slot * (R * kTensors) * threads;
+    const typename P::slot* at = slots + slot * (R * kTensors) * threads;
     Back<IO, VEC, ACT> v[R];
     P xr[R];
     float m1 = 0.f, m2 = 0.f;
@@ -114,9 +117,9 @@ __global__ void __launch_bounds__(LANES ? 256 : 512) row_bwd_kernel(
         const int64_t c = c0 + k * lanes * VEC;
         const Vals<VEC> wv = load_param<VEC>(w, c, 1.f);
         P dr, zr;
-        xr[k].r = at[k * kTensors * threads];
-        dr.r = at[(k * kTensors + 1) * threads];
-        if constexpr (kGated) zr.r = at[(k * kTensors + 2) * threads];
+        xr[k].take(at[k * kTensors * threads], x + n * p.sx + c);
+        dr.take(at[(k * kTensors + 1) * threads], dy + n * p.C + c);
+        if constexpr (kGated) zr.take(at[(k * kTensors + 2) * threads], z + n * p.sz + c);
         Vals<VEC> bv;
         if constexpr (ACT == SSD_NORM_SILU || ACT == SSD_NORM_GATE) bv = load_param<VEC>(bias, c, 0.f);
         v[k].from(xr[k], zr, dr, st.x, st.y, wv, bv);
@@ -164,9 +167,13 @@ __global__ void __launch_bounds__(LANES ? 256 : 512) row_bwd_kernel(
   grid_dep_launch();
 }
 
-// Packs of a group that a CTA of 512 threads holds
-constexpr int kMostPacks = 1024;
-bool rows_ok(const NormProblem& p, int vec) { return p.S == 1 && p.C / p.G / vec <= kMostPacks; }
+// Packs of `bytes` that a thread's registers and ring hold: 32 bytes of a tensor.  512 threads hold a group of 8192 bf16 or 4096
+// float32 channels whatever its rows' alignment is; a wider one goes through tiles of one position each, which leave a row
+// of shares a sample.  (12774 samples of 1337 bf16 channels: 642 us through tiles, 95 so.)
+constexpr int most_packs(int bytes) { return 32 / bytes; }
+bool rows_ok(const NormProblem& p, int vec) {
+  return p.S == 1 && p.C / p.G / vec <= 512 * most_packs(vec * (p.io_bf16 ? 2 : 4));
+}
 
 // How the rows are shared: threads of a CTA, lanes of a team (0: all), packs of a thread and samples taken at once.
 struct RowPlan {
@@ -175,10 +182,15 @@ struct RowPlan {
 };
 RowPlan row_plan(const NormProblem& p, int vec) {
   const int64_t items = p.C / p.G / vec;
-  RowPlan k{256, items <= 8 ? 8 : 32, items <= 32 ? 1 : 2, 0};
-  if (items > 64) k = RowPlan{round_up(items <= 512 ? items : ceil_div(items, 2), 32), 0, items <= 512 ? 1 : 2, 0};
-  // threads that an SM holds, by the registers of a pack or two; teams are a multiple of the groups
-  const int per_sm = 512 / k.threads < 1 ? 1 : 512 / k.threads;
+  const int most = most_packs(vec * (p.io_bf16 ? 2 : 4));
+  // A CTA's sums take barriers, but where there are fewer rows than SMs a row is done sooner by more threads (bf16, groups of
+  // 299 channels, warps against CTAs: 2804 x 4 rows 28 and 84 us, 200 rows 11.2 and 5.6 us).
+  const bool few = items > 64 && p.n * p.G <= 2 * kSMs;
+  RowPlan k{256, items <= 8 ? 8 : items <= 32 * most && !few ? 32 : 0, 1, 0};
+  while (items > (k.lanes ? k.lanes : 512) * k.R) k.R *= 2;
+  if (k.lanes == 0) k.threads = round_up(ceil_div(items, k.R), 32);
+  // threads that an SM holds, by the registers of their values; teams are a multiple of the groups
+  const int resident = k.R * vec <= 4 ? 1024 : 512, per_sm = resident / k.threads < 1 ? 1 : resident / k.threads;
   const int64_t fit = int64_t(kSMs) * per_sm * (k.lanes ? k.threads / k.lanes : 1) / p.G;
   k.stride = fit < 1 ? 1 : fit < p.n ? fit : p.n;
   return k;
@@ -188,7 +200,8 @@ template <typename IO, int VEC, int ACT, int R, int LANES>
 cudaError_t launch_rows(const NormProblem& p, const RowPlan& k, const IO* x, const IO* z, const float* w, const float* b,
                         const IO* dy, const float* mean, const float* rstd, IO* dx, IO* dz, float* shares, cudaStream_t st) {
   auto kern = row_bwd_kernel<IO, VEC, ACT, R, LANES>;
-  constexpr int kPerThread = R * (ACT == SSD_NORM_GATE || ACT == SSD_NORM_GATE_FIRST ? 3 : 2) * kRowSlots * Pack<IO, VEC>::kBytes;
+  constexpr int kBytes = R * Pack<IO, VEC>::kSlotBytes;
+  constexpr int kPerThread = (ACT == SSD_NORM_GATE || ACT == SSD_NORM_GATE_FIRST ? 3 : 2) * row_slots(kBytes) * kBytes;
   const cudaError_t e = allow_smem<row_bwd_kernel<IO, VEC, ACT, R, LANES>>(512 * kPerThread);
   if (e != cudaSuccess) return e;
   const int64_t ctas = ceil_div(k.stride * p.G, LANES ? k.threads / LANES : 1);
@@ -474,8 +487,19 @@ cudaError_t launch_group_norm_bwd(const NormProblem& p, const void* x, const voi
       const RowPlan k = row_plan(p, VEC);
 #define SSD_ROWS(RR, LL) launch_rows<IO, VEC, ACT, RR, LL>(p, k, xi, zi, w, b, di, mean, rstd, dxo, dzo, shares, st)
       if (k.lanes == 8) return SSD_ROWS(1, 8);
-      if (k.lanes == 32) return k.R == 1 ? SSD_ROWS(1, 32) : SSD_ROWS(2, 32);
-      return k.R == 1 ? SSD_ROWS(1, 0) : SSD_ROWS(2, 0);
+      constexpr int kMost = most_packs(Pack<IO, VEC>::kBytes);
+      if (k.R == 1) return k.lanes ? SSD_ROWS(1, 32) : SSD_ROWS(1, 0);
+      if (k.R == 2) return k.lanes ? SSD_ROWS(2, 32) : SSD_ROWS(2, 0);
+      if constexpr (kMost >= 4) {
+        if (k.R == 4) return k.lanes ? SSD_ROWS(4, 32) : SSD_ROWS(4, 0);
+      }
+      if constexpr (kMost >= 8) {
+        if (k.R == 8) return k.lanes ? SSD_ROWS(8, 32) : SSD_ROWS(8, 0);
+      }
+      if constexpr (kMost >= 16) {
+        if (k.R == 16) return k.lanes ? SSD_ROWS(16, 32) : SSD_ROWS(16, 0);
+      }
+      return cudaErrorInvalidConfiguration;  // rows_ok lets no larger group through
 #undef SSD_ROWS
     }
     const Cut k = cut_of(p, VEC);

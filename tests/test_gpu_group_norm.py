@@ -121,6 +121,30 @@ def test_tokens(dtype, n, C, G):
     check(inputs(n, 1, C, dtype, "gate_first", 3 + C), G, dtype, "gate_first", True)
 
 
+# wide groups whose rows take packs of one or two channels, with more samples than CTAs and with fewer
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,C,G", [(401, 1337, 1), (200, 2050, 2), (160, 2091, 1), (3, 2047, 1), (3, 2049, 1), (2, 4095, 1),
+                                   (2, 4097, 1), (161, 4098, 1), (2, 8190, 1), (2, 8191, 1), (2, 8193, 1)])
+def test_wide_odd_rows(dtype, n, C, G):
+    check(inputs(n, 1, C, dtype, "gate_first", 30 + C), G, dtype, "gate_first", False)
+    check(inputs(n, 1, C, dtype, "none", 31 + C), G, dtype, "none", True)
+
+
+# rows of single bf16 values at both offsets in a word; what lies around them is never taken in
+@pytest.mark.parametrize("n,C,G", [(1, 3, 3), (700, 72, 24), (33, 299, 1), (200, 416, 32), (5, 2051, 1), (3, 16382, 2),
+                                   (2, 16385, 1)])
+@pytest.mark.parametrize("at,more", [(0, 1), (1, 2), (3, 8)])
+def test_odd_rows(n, C, G, at, more):
+    for act in ("gate", "none"):
+        t = inputs(n, 1, C, "bf16", act, 40 + C + at)
+        for k in ("x", "z"):
+            if t[k] is not None:
+                wide = torch.full((n, 1, C + more), float("nan"), dtype=torch.bfloat16, device="cuda")
+                wide[:, :, at:at + C] = t[k]
+                t[k] = wide[:, :, at:at + C]
+        check(t, G, "bf16", act, False)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("n,S,C,G", [(1, 2, 1, 1), (2, 3, 5, 5), (2, 64, 64, 2), (3, 65, 64, 64), (2, 1000, 66, 11),
                                      (1, 4096, 64, 4), (5, 333, 320, 32), (2, 17, 2048, 1), (1, 20000, 48, 3),
